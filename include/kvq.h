@@ -79,6 +79,9 @@ typedef enum {
 #define KVQ_DEV_BAD_BLOCK 0x1u  /* a block-table entry outside [0, num_blocks) */
 #define KVQ_DEV_CAPACITY 0x2u   /* a sequence longer than the store can hold */
 #define KVQ_DEV_TIMEOUT 0x4u    /* a bounded wait for an asynchronous copy gave up */
+#define KVQ_DEV_BAD_TREE 0x8u   /* a parent, path entry, count or token outside its range */
+#define KVQ_DEV_RANGE 0x10u     /* tree attention: a query, Key or Value that f16 does not hold */
+#define KVQ_DEV_BAD_PROBS 0x20u /* a probability row without a positive finite sum */
 
 /* Per-layer configuration (host struct, read during the call only). */
 typedef struct {
@@ -429,6 +432,127 @@ kvq_status kvq_selftest_bounded_wait(const kvq_layer_config* cfg, const kvq_laye
                                      int32_t num_q_heads, const int32_t* seq_lens, int32_t batch,
                                      float softmax_scale, void* out, int32_t out_bf16, float* lse, void* workspace,
                                      size_t workspace_bytes, uint32_t* dev_status, void* stream);
+
+/*
+ * Speculative decoding over the cache: a step drafts a tree of tokens for every
+ * sequence, attends for all its nodes at once, verifies them against the target
+ * model's probabilities and appends the accepted path.  Rejected nodes never
+ * enter the cache, so a quantized group is never taken back.
+ *
+ * A tree has n_nodes nodes (1..64) per sequence; node 0 is the root: the last
+ * token of the sequence that is not in the cache yet.  parents is device int32
+ * [batch][n_nodes]: parents[n] < n, or -1 for a node without one (node 0 has
+ * none).  A sequence with fewer drafted tokens pads its tree with nodes of
+ * parent -1.  An entry outside [-1, n) counts as -1 (KVQ_DEV_BAD_TREE).  A node's
+ * position is the sequence's length plus its depth.
+ */
+
+/*
+ * kvq_qk_norm_rope -- what a layer does between the fused projection and the
+ * cache: queries and keys normed per head and rotated to their positions, keys
+ * and values laid out for kvq_quantize_append (and the tree calls below).
+ * Source: [KVQA] s3 (Keys and RoPE: the rotation comes before or after the
+ * quantization) and s5 (K and V right after they are computed).
+ *   qkv         device bf16, batch * n_tokens rows of (num_q_heads + 2 num_kv_heads)
+ *               heads of 128 (queries, keys, values), row_stride elements from one
+ *               row to the next (a multiple of 8, at least a row), 16-byte aligned
+ *   q_weight, k_weight  device bf16 [128], or NULL: not normed.  A head x becomes
+ *               w x / sqrt(mean(x^2) + eps)  (eps >= 0, finite)
+ *   positions   device int32 [batch][n_tokens]; NULL with rope_base == 0
+ *   rope_base   > 1: queries are rotated as kvq_layer_config.rope_base describes
+ *               (pair i, i + 64 by position * rope_base^(-2i/128)); 0: not rotated
+ *   rotate_keys 1: keys are rotated as the queries are; 0: they are left as they are
+ *               (layers with pre-RoPE Keys)
+ *   q_out       device bf16 [batch][n_tokens][num_q_heads][128]
+ *   k_out, v_out  device bf16 [batch][num_kv_heads][n_tokens][128]; values are copied
+ * All outputs 16-byte aligned, none overlapping qkv.  Computed in fp32 (angles
+ * reduced exactly in 64-bit fixed point) and rounded once.
+ */
+kvq_status kvq_qk_norm_rope(const void* qkv, int64_t row_stride, int32_t batch, int32_t n_tokens,
+                            int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, const void* q_weight,
+                            const void* k_weight, float eps, const int32_t* positions, float rope_base,
+                            int32_t rotate_keys, void* q_out, void* k_out, void* v_out, void* stream);
+
+/*
+ * kvq_decode_attention_tree -- attention of a tree's nodes over the quantized
+ * cache.  Source: [W4KV] "오차가 어디서 만나는가" (the score formula) with a
+ * node seeing every cached token of its sequence, its ancestors and itself.
+ *   q         device bf16 [batch][n_nodes][num_q_heads][d], 16-byte aligned,
+ *             rotated to the nodes' positions
+ *   k_draft, v_draft  device bf16 [batch][H][n_nodes][d], 16-byte aligned: the
+ *             nodes' own keys and values, read from here (they are not in the cache)
+ *   seq_lens  device int32 [batch]: tokens in the cache (the tree not among them)
+ *   out       device [batch][n_nodes][num_q_heads][d] (fp32 or bf16 as above)
+ *   lse       device f32 [batch][n_nodes][num_q_heads] or NULL
+ *   workspace at least kvq_decode_workspace_size_tree() bytes, 16-byte aligned,
+ *             zero-filled once before first use (arrival counters, as for
+ *             kvq_decode_attention)
+ * num_q_heads / H <= 8.  Pre-RoPE and dense-and-sparse layers are not supported
+ * (KVQ_ERR_UNSUPPORTED).  The tensor cores take f16 operands: a query, Key or
+ * Value that is not finite or that f16 does not hold (beyond +-65504; FP8 layers:
+ * Values beyond 65504 tensor scales, E5M2: 256 times that) is reported as
+ * KVQ_DEV_RANGE, and the rows that see it are not valid; rows of nodes that do not
+ * see it are.  Other errors as for kvq_decode_attention.
+ */
+kvq_status kvq_decode_attention_tree(const kvq_layer_config* cfg, const kvq_layer_cache* cache, const void* q,
+                                     const void* k_draft, const void* v_draft, const int32_t* parents,
+                                     int32_t n_nodes, int32_t num_q_heads, const int32_t* seq_lens, int32_t batch,
+                                     float softmax_scale, void* out, int32_t out_bf16, float* lse, void* workspace,
+                                     size_t workspace_bytes, uint32_t* dev_status, void* stream);
+
+/* Workspace bytes kvq_decode_attention_tree needs on the current device. */
+kvq_status kvq_decode_workspace_size_tree(const kvq_layer_config* cfg, int32_t batch, int32_t n_nodes,
+                                          int32_t num_q_heads, size_t* bytes);
+
+/*
+ * kvq_verify_tree -- which drafted nodes the target model accepts, and the next
+ * token, so that the tokens are distributed as the target's own (no counterpart
+ * in the pages).
+ *   target_probs device f32, batch * n_nodes rows of vocab probabilities: row n of a
+ *             sequence is the target's distribution after node n.  target_stride
+ *             elements (>= vocab) from one row to the next
+ *   draft_probs  the same for the drafter (draft_stride): node n's children were
+ *             drawn from row n, each independently.  NULL: the children were chosen,
+ *             not drawn (the drafter's distribution is all on the child's token)
+ *   tokens    device int32 [batch][n_nodes]: the nodes' tokens (node 0's is not read)
+ *   parents   device int32 [batch][n_nodes] (see above)
+ *   uniforms  device f32 [batch][n_nodes]: numbers in [0, 1); entry n > 0 decides
+ *             node n, entry 0 draws the next token
+ *   path      device int32 [batch][n_nodes]: the accepted nodes from the root down,
+ *             then -1;  n_accepted device int32 [batch]: how many (the root counts);
+ *   next_token device int32 [batch]
+ * From the root: with w = target row and W = 1, the children c of the last
+ * accepted node are tried in index order; token x of c is accepted when
+ * uniforms[c] * W * q(x) < w(x) (q: the drafter's row), and otherwise
+ * w <- max(w - W q, 0), W <- sum(w).  When no child is left the next token is the
+ * first with cumsum(w) > uniforms[0] * sum(w) (the last with w > 0 if there is
+ * none).  A w that is 0 everywhere at the end is replaced by the target row.
+ * Sums are carried in pairs of fp32 numbers (about 45 bits) in a fixed order.  A
+ * token outside [0, vocab) is not accepted (KVQ_DEV_BAD_TREE); a target row without
+ * a positive finite sum gives next_token = -1 (KVQ_DEV_BAD_PROBS).
+ */
+kvq_status kvq_verify_tree(const float* target_probs, int64_t target_stride, const float* draft_probs,
+                           int64_t draft_stride, int32_t vocab, const int32_t* tokens, const int32_t* parents,
+                           const float* uniforms, int32_t n_nodes, int32_t batch, int32_t* path,
+                           int32_t* n_accepted, int32_t* next_token, uint32_t* dev_status, void* stream);
+
+/*
+ * kvq_append_accepted -- append the accepted nodes' keys and values: for every
+ * sequence the rows path[b][0 .. n_accepted[b]) of the drafted tokens, in that
+ * order.  Source: as kvq_quantize_append, whose result for the same rows it equals.
+ *   k_draft, v_draft  device bf16 [batch][H][n_nodes][d], 16-byte aligned
+ *   path      device int32 [batch][n_nodes], entries in [0, n_nodes)
+ *   n_accepted device int32 [batch], 0 .. n_nodes (0: nothing is appended)
+ *   seq_lens  device int32 [batch]: tokens in the cache before the call
+ * The caller advances seq_lens by n_accepted afterwards, and for a paged store has
+ * the blocks of every group that spills already in the block table.
+ * Device errors: those of kvq_quantize_append; KVQ_DEV_BAD_TREE (a count or an
+ * entry outside its range: nothing is written for that sequence).
+ */
+kvq_status kvq_append_accepted(const kvq_layer_config* cfg, const kvq_layer_cache* cache, const void* k_draft,
+                               const void* v_draft, int32_t n_nodes, const int32_t* path,
+                               const int32_t* n_accepted, const int32_t* seq_lens, int32_t batch,
+                               uint32_t* dev_status, void* stream);
 
 /* Human-readable name of a status code (static string). */
 const char* kvq_status_string(kvq_status status);

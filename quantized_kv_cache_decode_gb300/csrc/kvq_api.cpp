@@ -360,6 +360,8 @@ kvq_status kvq_quantize_append(const kvq_layer_config* cfg, const kvq_layer_cach
   p.batch = batch;
   p.seq_lens = seq_lens;
   p.status = dev_status;
+  p.path = nullptr;
+  p.counts = nullptr;
   if (launch_append(p, static_cast<cudaStream_t>(stream)) != cudaSuccess) return KVQ_ERR_CUDA;
   return KVQ_OK;
 }
@@ -641,6 +643,231 @@ kvq_status kvq_lse_merge(const float* o_parts, const float* lse_parts, int32_t n
       cudaSuccess)
     return KVQ_ERR_CUDA;
   return KVQ_OK;
+}
+
+kvq_status kvq_append_accepted(const kvq_layer_config* cfg, const kvq_layer_cache* cache, const void* k_draft,
+                               const void* v_draft, int32_t n_nodes, const int32_t* path,
+                               const int32_t* n_accepted, const int32_t* seq_lens, int32_t batch,
+                               uint32_t* dev_status, void* stream) {
+  LayerDesc L;
+  kvq_status st = make_desc(cfg, &L);
+  if (st != KVQ_OK) return st;
+  if ((st = check_cache(L, cache)) != KVQ_OK) return st;
+  if (batch < 0 || batch > kMaxBatch || n_nodes < 1 || n_nodes > kMaxNodes) return KVQ_ERR_INVALID_ARG;
+  if (batch == 0) return KVQ_OK;
+  if (!k_draft || !v_draft || !path || !n_accepted || !seq_lens || !aligned16(k_draft) || !aligned16(v_draft))
+    return KVQ_ERR_INVALID_ARG;
+  AppendParams p;
+  p.L = L;
+  p.C = make_ptrs(cache);
+  p.k_new = k_draft;
+  p.v_new = v_draft;
+  p.n_new = n_nodes;
+  p.batch = batch;
+  p.seq_lens = seq_lens;
+  p.status = dev_status;
+  p.path = path;
+  p.counts = n_accepted;
+  return launch_append(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+}
+
+kvq_status kvq_qk_norm_rope(const void* qkv, int64_t row_stride, int32_t batch, int32_t n_tokens,
+                            int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, const void* q_weight,
+                            const void* k_weight, float eps, const int32_t* positions, float rope_base,
+                            int32_t rotate_keys, void* q_out, void* k_out, void* v_out, void* stream) {
+  if (head_dim != kHeadDim) return KVQ_ERR_UNSUPPORTED;
+  if (batch < 0 || n_tokens < 0 || num_q_heads < 1 || num_kv_heads < 1 || num_q_heads > (1 << 16) ||
+      num_kv_heads > (1 << 16))
+    return KVQ_ERR_INVALID_ARG;
+  const int64_t row = ((int64_t)num_q_heads + 2 * (int64_t)num_kv_heads) * kHeadDim;
+  if (row_stride < row || row_stride % 8 != 0 || row_stride > ((int64_t)1 << 40)) return KVQ_ERR_INVALID_ARG;
+  if (!(eps >= 0.f) || !(eps < 3.0e38f)) return KVQ_ERR_INVALID_ARG;
+  if (rotate_keys != 0 && rotate_keys != 1) return KVQ_ERR_INVALID_ARG;
+  if (rope_base != 0.f && (!(rope_base > 1.f) || !(rope_base < 3.0e38f))) return KVQ_ERR_INVALID_ARG;
+  if (batch == 0 || n_tokens == 0) return KVQ_OK;
+  if (!qkv || !q_out || !k_out || !v_out || !aligned16(qkv) || !aligned16(q_out) || !aligned16(k_out) ||
+      !aligned16(v_out) || (rope_base != 0.f && !positions))
+    return KVQ_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(q_weight) & 15u) || (reinterpret_cast<uintptr_t>(k_weight) & 15u))
+    return KVQ_ERR_INVALID_ARG;
+  NormRopeParams p;
+  p.qkv = qkv;
+  p.row_stride = row_stride;
+  p.n_tokens = n_tokens;
+  p.Hq = num_q_heads;
+  p.H = num_kv_heads;
+  p.rows = (long long)batch * n_tokens;
+  p.q_weight = q_weight;
+  p.k_weight = k_weight;
+  p.eps = eps;
+  p.positions = positions;
+  p.rotate = rope_base != 0.f;
+  p.rotate_keys = p.rotate && rotate_keys;
+  p.q_out = q_out;
+  p.k_out = k_out;
+  p.v_out = v_out;
+  if (p.rotate) {
+    // theta_i = base^(-i/64) from six square roots and at most six products (a pow per pair would
+    // cost more than the launch); a relative error of a few 2^-53, as the table's own rounding
+    double f[6];
+    f[5] = 1.0 / std::sqrt((double)rope_base);  // base^(-32/64)
+    for (int j = 4; j >= 0; --j) f[j] = std::sqrt(f[j + 1]);
+    for (int i = 0; i < 64; ++i) {
+      double theta = 1.0;
+      for (int j = 0; j < 6; ++j)
+        if ((i >> j) & 1) theta *= f[j];
+      const double turn = theta / (2.0 * 3.14159265358979323846);  // < 1
+      p.turn[i] = (unsigned long long)(turn * 18446744073709551616.0);
+    }
+  }
+  return launch_norm_rope(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+}
+
+kvq_status kvq_verify_tree(const float* target_probs, int64_t target_stride, const float* draft_probs,
+                           int64_t draft_stride, int32_t vocab, const int32_t* tokens, const int32_t* parents,
+                           const float* uniforms, int32_t n_nodes, int32_t batch, int32_t* path,
+                           int32_t* n_accepted, int32_t* next_token, uint32_t* dev_status, void* stream) {
+  if (vocab < 1 || n_nodes < 1 || n_nodes > kMaxNodes || batch < 0 || batch > kMaxBatch) return KVQ_ERR_INVALID_ARG;
+  if (target_stride < vocab || target_stride > ((int64_t)1 << 40)) return KVQ_ERR_INVALID_ARG;
+  if (draft_probs && (draft_stride < vocab || draft_stride > ((int64_t)1 << 40))) return KVQ_ERR_INVALID_ARG;
+  if (batch == 0) return KVQ_OK;
+  if (!target_probs || !tokens || !parents || !uniforms || !path || !n_accepted || !next_token)
+    return KVQ_ERR_INVALID_ARG;
+  VerifyParams p;
+  p.target = target_probs;
+  p.draft = draft_probs;
+  p.tstride = target_stride;
+  p.dstride = draft_stride;
+  p.V = vocab;
+  p.N = n_nodes;
+  p.batch = batch;
+  p.tokens = tokens;
+  p.parents = parents;
+  p.uniforms = uniforms;
+  p.path = path;
+  p.n_accepted = n_accepted;
+  p.next_token = next_token;
+  p.status = dev_status;
+  return launch_verify(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+}
+
+}  // extern "C"
+
+namespace kvq {
+namespace {
+
+struct TreeGeom {
+  int sub, chunks, ctas, smem, nslots, slot_bytes, slot_hdr, bf_tokens;
+  size_t off_ml, off_counters, ws_bytes;
+};
+
+// Launch shape of the tree attention: the narrowest column halves that hold all columns in one
+// chunk (64-column halves and several chunks beyond 128), one CTA per SM, as many slots as fit.
+kvq_status tree_geometry(const LayerDesc& L, int batch, int columns, TreeGeom* G) {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return KVQ_ERR_CUDA;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return KVQ_ERR_CUDA;
+  G->sub = columns <= 32 ? 16 : (columns <= 64 ? 32 : 64);
+  G->chunks = (columns + 2 * G->sub - 1) / (2 * G->sub);
+  G->ctas = sms;
+  // a quantized slot: 64 tokens, the headers of the records that they touch first
+  int headers = 0;
+  if (!L.fp8 && !L.bf16) headers = L.tpg == 1 ? 4 : (L.tpg % 4 == 0 ? 1 : 2);
+  G->slot_hdr = headers * 1024;
+  const int need = L.bf16 ? 0 : G->slot_hdr + 4 * L.tile_bytes;
+  G->slot_bytes = (std::max(need, L.bf16 ? 32768 : 16384) + 127) / 128 * 128;
+  G->bf_tokens = G->slot_bytes >= 32768 ? 64 : 32;
+  const size_t fixed = tree_fixed_smem(G->sub, batch);
+  const size_t budget = 227 * 1024;
+  if (fixed + 2 * (size_t)G->slot_bytes > budget) return KVQ_ERR_UNSUPPORTED;
+  G->nslots = (int)std::min<size_t>(12, (budget - fixed) / G->slot_bytes);
+  G->smem = (int)(fixed + (size_t)G->nslots * G->slot_bytes);
+  const size_t rows = 2 * (size_t)G->ctas * 2 * G->sub;
+  G->off_ml = rows * kHeadDim * sizeof(float);
+  G->off_counters = G->off_ml + rows * 2 * sizeof(float);
+  G->ws_bytes = G->off_counters + (size_t)batch * L.H * G->chunks * sizeof(unsigned);
+  return KVQ_OK;
+}
+
+kvq_status check_tree_args(const kvq_layer_config* cfg, int32_t n_nodes, int32_t num_q_heads, int32_t batch,
+                           LayerDesc* L) {
+  kvq_status st = check_decode_args(cfg, num_q_heads, batch, L);
+  if (st != KVQ_OK) return st;
+  if (n_nodes < 1 || n_nodes > kMaxNodes) return KVQ_ERR_INVALID_ARG;
+  if (L->rope || L->k_out || L->v_out) return KVQ_ERR_UNSUPPORTED;
+  return KVQ_OK;
+}
+
+}  // namespace
+}  // namespace kvq
+
+extern "C" {
+
+kvq_status kvq_decode_workspace_size_tree(const kvq_layer_config* cfg, int32_t batch, int32_t n_nodes,
+                                          int32_t num_q_heads, size_t* bytes) {
+  LayerDesc L;
+  kvq_status st = check_tree_args(cfg, n_nodes, num_q_heads, batch, &L);
+  if (st != KVQ_OK) return st;
+  if (!bytes) return KVQ_ERR_INVALID_ARG;
+  TreeGeom G;
+  if ((st = tree_geometry(L, batch, num_q_heads / L.H * n_nodes, &G)) != KVQ_OK) return st;
+  *bytes = G.ws_bytes;
+  return KVQ_OK;
+}
+
+kvq_status kvq_decode_attention_tree(const kvq_layer_config* cfg, const kvq_layer_cache* cache, const void* q,
+                                     const void* k_draft, const void* v_draft, const int32_t* parents,
+                                     int32_t n_nodes, int32_t num_q_heads, const int32_t* seq_lens, int32_t batch,
+                                     float softmax_scale, void* out, int32_t out_bf16, float* lse, void* workspace,
+                                     size_t workspace_bytes, uint32_t* dev_status, void* stream) {
+  LayerDesc L;
+  kvq_status st = check_tree_args(cfg, n_nodes, num_q_heads, batch, &L);
+  if (st != KVQ_OK) return st;
+  if (out_bf16 != 0 && out_bf16 != 1) return KVQ_ERR_INVALID_ARG;
+  if ((st = check_cache(L, cache)) != KVQ_OK) return st;
+  if (batch == 0) return KVQ_OK;
+  if (!q || !k_draft || !v_draft || !parents || !seq_lens || !out || !workspace || !aligned16(q) ||
+      !aligned16(k_draft) || !aligned16(v_draft) || !aligned16(workspace) || !(softmax_scale == softmax_scale))
+    return KVQ_ERR_INVALID_ARG;
+  TreeGeom G;
+  if ((st = tree_geometry(L, batch, num_q_heads / L.H * n_nodes, &G)) != KVQ_OK) return st;
+  if (workspace_bytes < G.ws_bytes) return KVQ_ERR_WORKSPACE;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  TreeParams p;
+  p.L = L;
+  p.C = make_ptrs(cache);
+  p.q = q;
+  p.k_draft = k_draft;
+  p.v_draft = v_draft;
+  p.parents = parents;
+  p.seq_lens = seq_lens;
+  p.N = n_nodes;
+  p.Hq = num_q_heads;
+  p.gh = num_q_heads / L.H;
+  p.batch = batch;
+  p.chunks = G.chunks;
+  p.nslots = G.nslots;
+  p.slot_bytes = G.slot_bytes;
+  p.slot_hdr = G.slot_hdr;
+  p.bf_tokens = G.bf_tokens;
+  p.scale_log2 = softmax_scale * 1.4426950408889634f;
+  p.ws_o = reinterpret_cast<float*>(ws);
+  p.ws_ml = reinterpret_cast<float*>(ws + G.off_ml);
+  p.counters = reinterpret_cast<unsigned*>(ws + G.off_counters);
+  p.status = dev_status;
+  p.out = out;
+  p.out_bf16 = out_bf16;
+  p.lse = lse;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  switch (kernel_format(L.fmt)) {
+    case KVQ_FMT_INT2: e = launch_tree_int2(p, G.sub, G.ctas, G.smem, s); break;
+    case KVQ_FMT_INT4: e = launch_tree_int4(p, G.sub, G.ctas, G.smem, s); break;
+    case KVQ_FMT_INT8: e = launch_tree_int8(p, G.sub, G.ctas, G.smem, s); break;
+    case KVQ_FMT_FP8_E5M2: e = launch_tree_fp8_e5m2(p, G.sub, G.ctas, G.smem, s); break;
+    default: e = launch_tree_fp8(p, G.sub, G.ctas, G.smem, s); break;
+  }
+  return e == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
 }
 
 const char* kvq_status_string(kvq_status status) {

@@ -40,9 +40,35 @@ __device__ __forceinline__ uint8_t* record_w(const LayerDesc& L, const CachePtrs
   return const_cast<uint8_t*>(record_addr(L, C, b, h, r, status));
 }
 
+// Rows that sequence b appends (PATH: kvq_append_accepted): n, or -1 (reported) when the count or an
+// entry of the path is outside its range.  Called by the whole CTA.
+template <bool PATH>
+__device__ __forceinline__ int append_rows(const AppendParams& p, int b, bool tell) {
+  if constexpr (!PATH) return p.n_new;
+  const int n = p.counts[b];
+  bool bad = n < 0 || n > p.n_new;
+  if (!bad)
+    for (int j = threadIdx.x; j < n; j += blockDim.x) {
+      const int r = p.path[(long long)b * p.n_new + j];
+      bad |= r < 0 || r >= p.n_new;
+    }
+  if (__syncthreads_or(bad)) {
+    if (tell) report(p.status, KVQ_DEV_BAD_TREE);
+    return -1;
+  }
+  return n;
+}
+// the input row of the j-th appended token
+template <bool PATH>
+__device__ __forceinline__ long long append_row(const AppendParams& p, int b, long long j) {
+  if constexpr (!PATH) return j;
+  return p.path[(long long)b * p.n_new + j];
+}
+
 // One CTA per (sequence, kv head): FP8 tokens (encoded one by one), bf16 rows of
 // the residual window (integer layers: only the tokens that stay there after the
 // groups that spill, which spill_kernel quantizes) and sink rows.
+template <bool PATH>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendParams p) {
   pdl_wait();  // the previous kernel of the stream has finished (programmatic launch)
   pdl_trigger();
@@ -50,8 +76,10 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
   const int b = blockIdx.x / L.H, h = blockIdx.x % L.H;
   const int tid = threadIdx.x;
   const long long pair = (long long)b * L.H + h;
+  const int n_new = append_rows<PATH>(p, b, h == 0 && tid == 0);
+  if (n_new < 0) return;
   const long long T0 = p.seq_lens[b];
-  const long long T1 = T0 + p.n_new;
+  const long long T1 = T0 + n_new;
   if (T0 < 0 || T1 > max_tokens(L)) {
     if (tid == 0) report(p.status, KVQ_DEV_CAPACITY);
     return;
@@ -82,8 +110,8 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
       }
       const int c = tid;
       const int tt = (int)(x % 16);
-      const float kx = __bfloat162float(knew[(t - T0) * L.d + c]);
-      const float vx = __bfloat162float(vnew[(t - T0) * L.d + c]);
+      const float kx = __bfloat162float(knew[append_row<PATH>(p, b, t - T0) * L.d + c]);
+      const float vx = __bfloat162float(vnew[append_row<PATH>(p, b, t - T0) * L.d + c]);
       int byte, bit;
       const float kd = __fdiv_rn(kx, sk), vd = __fdiv_rn(vx, sv);
       ktile_pos(8, true, tt, c, byte, bit);
@@ -98,15 +126,15 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
     for (long long t = rfirst; t < T1; ++t) {
       const long long slot = (t - L.S) % L.W;
       const int c = tid;
-      ring_k[(pair * L.W + slot) * L.d + c] = knew[(t - T0) * L.d + c];
-      ring_v[(pair * L.W + slot) * L.d + c] = vnew[(t - T0) * L.d + c];
+      ring_k[(pair * L.W + slot) * L.d + c] = knew[append_row<PATH>(p, b, t - T0) * L.d + c];
+      ring_v[(pair * L.W + slot) * L.d + c] = vnew[append_row<PATH>(p, b, t - T0) * L.d + c];
     }
   }
   // sink tokens
   for (long long t = T0; t < T1 && t < L.S; ++t) {
     const int c = tid;
-    sink_k[(pair * L.S + t) * L.d + c] = knew[(t - T0) * L.d + c];
-    sink_v[(pair * L.S + t) * L.d + c] = vnew[(t - T0) * L.d + c];
+    sink_k[(pair * L.S + t) * L.d + c] = knew[append_row<PATH>(p, b, t - T0) * L.d + c];
+    sink_v[(pair * L.S + t) * L.d + c] = vnew[append_row<PATH>(p, b, t - T0) * L.d + c];
   }
 }
 
@@ -149,7 +177,7 @@ __device__ __forceinline__ void frag_field(int w, int bp, int& step, int& reg, i
   }
 }
 
-template <int BITS, int NT>
+template <int BITS, int NT, bool PATH>
 __global__ void __launch_bounds__(NT, 1024 / NT) spill_kernel(const AppendParams p, int rest) {
   pdl_wait();  // the previous kernel of the stream has finished (programmatic launch)
   pdl_trigger();
@@ -162,11 +190,13 @@ __global__ void __launch_bounds__(NT, 1024 / NT) spill_kernel(const AppendParams
   constexpr int kWPart = 16 * kRB / 4;       // operand words of one code matrix
   constexpr int kFields = 32 / BITS;         // codes per word
   const int b = blockIdx.x / L.H, h = blockIdx.x % L.H;
-  const int gi = blockIdx.y;
+  int gi = blockIdx.y;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const long long pair = (long long)b * L.H + h;
+  const int n_new = append_rows<PATH>(p, b, h == 0 && gi == 0 && tid == 0);
+  if (n_new < 0) return;
   const long long T0 = p.seq_lens[b];
-  const long long T1 = T0 + p.n_new;
+  const long long T1 = T0 + n_new;
   if (T0 < 0 || T1 > max_tokens(L)) {
     if (gi == 0 && tid == 0) report(p.status, KVQ_DEV_CAPACITY);
     return;
@@ -180,7 +210,10 @@ __global__ void __launch_bounds__(NT, 1024 / NT) spill_kernel(const AppendParams
   const int G = L.G, ngv = L.ngv, Gv = L.Gv;
   const int ng = (t1s.qn - t0s.qn) / G;  // groups that spill in this call
 
-  if (gi < ng) {
+  // one group per CTA; with a path (at most kMaxNodes rows, rarely a group) one CTA takes them all,
+  // so that it may write the rows that stay in the window behind them
+  for (; gi < ng; gi += PATH ? 1 : ng) {
+    if (PATH && gi > 0) __syncthreads();
     const int grp = t0s.qn / G + gi;
     const long long x0 = (long long)grp * G;  // first quantized index of the group
     uint8_t* rec = record_w(L, p.C, b, h, grp, tid == 0 ? p.status : nullptr);
@@ -209,7 +242,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) spill_kernel(const AppendParams
               if (sl >= L.W) sl -= L.W;
               src = (which ? ring_v : ring_k) + (pair * L.W + sl) * L.d;
             } else {
-              src = (which ? vnew : knew) + (t - T0) * L.d;
+              src = (which ? vnew : knew) + append_row<PATH>(p, b, t - T0) * L.d;
             }
             v[u] = reinterpret_cast<const uint4*>(src)[ch];
           }
@@ -383,7 +416,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) spill_kernel(const AppendParams
       }
     }
   }
-  if (rest && gi == 0) {
+  if (rest && blockIdx.y == 0) {
+    if (PATH) __syncthreads();  // (the ring rows that spill have been read)
     // sink rows, and the new rows that stay in the residual window (16-byte chunks)
     __nv_bfloat16* sink_k = reinterpret_cast<__nv_bfloat16*>(p.C.sink_k);
     __nv_bfloat16* sink_v = reinterpret_cast<__nv_bfloat16*>(p.C.sink_v);
@@ -392,7 +426,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) spill_kernel(const AppendParams
     for (int idx = tid; idx < 2 * n * 16; idx += NT) {
       const int which = idx >= n * 16, rem = idx - which * n * 16, j = rem >> 4, ch = rem & 15;
       const long long t = T0 + j;
-      const __nv_bfloat16* src = (which ? vnew : knew) + (long long)j * L.d;
+      const __nv_bfloat16* src = (which ? vnew : knew) + append_row<PATH>(p, b, j) * L.d;
       __nv_bfloat16* dst = nullptr;
       if (t < L.S) dst = (which ? sink_v : sink_k) + (pair * L.S + t) * L.d;
       else if (t >= rfirst) dst = (which ? ring_v : ring_k) + (pair * L.W + (t - L.S) % L.W) * L.d;
@@ -401,7 +435,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) spill_kernel(const AppendParams
   }
 }
 
-template <int BITS, int NT>
+template <int BITS, int NT, bool PATH>
 cudaError_t launch_spill_nt(const AppendParams& p, int groups, int rest, cudaStream_t stream) {
   const size_t smem =
       (size_t)p.L.G * kSRow * 2 * 2 + (256 + (NT / 128) * 256) * 4 + (size_t)p.L.G * p.L.ngv * 8;
@@ -413,12 +447,12 @@ cudaError_t launch_spill_nt(const AppendParams& p, int groups, int rest, cudaStr
   {
     std::lock_guard<std::mutex> lock(mu);
     if (dev < 0 || dev >= 64 || set_for[dev] < (int)smem) {
-      e = cudaFuncSetAttribute(spill_kernel<BITS, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      e = cudaFuncSetAttribute(spill_kernel<BITS, NT, PATH>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
       if (e != cudaSuccess) return e;
       if (dev >= 0 && dev < 64) set_for[dev] = (int)smem;
     }
   }
-  return launch_pdl(spill_kernel<BITS, NT>, dim3(p.batch * p.L.H, groups), dim3(NT), smem, stream, p, rest);
+  return launch_pdl(spill_kernel<BITS, NT, PATH>, dim3(p.batch * p.L.H, groups), dim3(NT), smem, stream, p, rest);
 }
 
 // Threads per spill CTA: few CTAs (one group per sequence and head, few pairs) get
@@ -426,36 +460,42 @@ cudaError_t launch_spill_nt(const AppendParams& p, int groups, int rest, cudaStr
 // passes are short.  Measured on GB300: the 70B INT4 layer's spill (128 CTAs of a
 // 128-token group) 41 -> 26 us from 256 to 1024 threads, the INT2 MHA layer's
 // (1024 CTAs of a 32-token group) 37 -> 76 us the other way.
-template <int BITS>
+template <int BITS, bool PATH>
 cudaError_t launch_spill_t(const AppendParams& p, int groups, int rest, cudaStream_t stream) {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return cudaErrorInvalidDevice;
   const long long ctas = (long long)p.batch * p.L.H * groups;
   if constexpr (BITS != 2) {  // (2-bit words hold 16 codes: the 1024-thread form would spill registers)
-    if (ctas <= 2LL * sms) return launch_spill_nt<BITS, 1024>(p, groups, rest, stream);
+    if (ctas <= 2LL * sms) return launch_spill_nt<BITS, 1024, PATH>(p, groups, rest, stream);
   }
-  if (ctas <= 4LL * sms) return launch_spill_nt<BITS, 512>(p, groups, rest, stream);
-  return launch_spill_nt<BITS, 256>(p, groups, rest, stream);
+  if (ctas <= 4LL * sms) return launch_spill_nt<BITS, 512, PATH>(p, groups, rest, stream);
+  return launch_spill_nt<BITS, 256, PATH>(p, groups, rest, stream);
+}
+
+template <bool PATH>
+cudaError_t launch_spill(const AppendParams& p, int groups, int rest, cudaStream_t stream) {
+  switch (p.L.bits) {
+    case 2: return launch_spill_t<2, PATH>(p, groups, rest, stream);
+    case 4: return launch_spill_t<4, PATH>(p, groups, rest, stream);
+    default: return launch_spill_t<8, PATH>(p, groups, rest, stream);
+  }
 }
 
 cudaError_t launch_append(const AppendParams& p, cudaStream_t stream) {
   const int blocks = p.batch * p.L.H;
   if (blocks == 0 || p.n_new == 0) return cudaSuccess;
   if (p.L.fp8 || p.L.bf16) {
-    return launch_pdl(append_kernel, dim3(blocks), dim3(kAppendThreads), 0, stream, p);
+    return p.path ? launch_pdl(append_kernel<true>, dim3(blocks), dim3(kAppendThreads), 0, stream, p)
+                  : launch_pdl(append_kernel<false>, dim3(blocks), dim3(kAppendThreads), 0, stream, p);
   }
+  if (p.path) return launch_spill<true>(p, 1, 1, stream);  // spills, window and sink rows in one launch
   // integer layers: at most ceil(n_new / G) groups spill per (sequence, head)
   const int groups = (int)(((long long)p.n_new + p.L.G - 1) / p.L.G);
   const int fused = p.n_new == 1;  // one new token: its row never aliases a ring row the spill reads
-  cudaError_t e;
-  switch (p.L.bits) {
-    case 2: e = launch_spill_t<2>(p, groups, fused, stream); break;
-    case 4: e = launch_spill_t<4>(p, groups, fused, stream); break;
-    default: e = launch_spill_t<8>(p, groups, fused, stream); break;
-  }
+  const cudaError_t e = launch_spill<false>(p, groups, fused, stream);
   if (e != cudaSuccess || fused) return e;
-  return launch_pdl(append_kernel, dim3(blocks), dim3(kAppendThreads), 0, stream, p);  // window and sink rows after the spills
+  return launch_pdl(append_kernel<false>, dim3(blocks), dim3(kAppendThreads), 0, stream, p);  // window and sink rows after the spills
 }
 
 // ---------------------------------------------------------------------------

@@ -106,6 +106,36 @@ struct CombineParams {
   float* lse;
 };
 
+// kvq_decode_attention_tree (kvq_tree.cuh)
+struct TreeParams {
+  LayerDesc L;
+  CachePtrs C;
+  const void* q;        // bf16 [B][N][Hq][d]
+  const void* k_draft;  // bf16 [B][H][N][d]
+  const void* v_draft;
+  const int32_t* parents;  // [B][N]
+  const int32_t* seq_lens;
+  int N, Hq, gh, batch;
+  int chunks;      // column chunks of 2 * SUB per (sequence, kv head)
+  int nslots, slot_bytes;
+  int slot_hdr;    // bytes of record headers at the start of a quantized slot
+  int bf_tokens;   // bf16 tokens per slot (K rows, then V rows)
+  float scale_log2;
+  float* ws_o;     // [2 per CTA][2 * SUB][d] unnormalised partial outputs
+  float* ws_ml;    // [2 per CTA][2 * SUB][2] maximum (log2 domain) and sum
+  unsigned* counters;  // [B * H * chunks], zero between calls
+  uint32_t* status;
+  void* out;
+  int out_bf16;
+  float* lse;
+};
+
+// CTAs that share a tree launch's blocks: all of them, at least one block each
+__host__ __device__ inline long long tree_ctas(long long grid, long long blocks) {
+  return blocks < grid ? (blocks < 1 ? 1 : blocks) : grid;
+}
+constexpr int kMaxNodes = 64;  // nodes of a tree: one bit each in the ancestor masks
+
 struct AppendParams {
   LayerDesc L;
   CachePtrs C;
@@ -113,6 +143,40 @@ struct AppendParams {
   const void* v_new;
   int n_new, batch;
   const int32_t* seq_lens;
+  uint32_t* status;
+  // kvq_append_accepted: sequence b appends rows path[b][0 .. counts[b]) of its n_new rows
+  // (NULL: all of them, in order)
+  const int32_t* path;
+  const int32_t* counts;
+};
+
+struct NormRopeParams {
+  const void* qkv;
+  long long row_stride;
+  int n_tokens, Hq, H;
+  long long rows;          // batch * n_tokens
+  const void* q_weight;
+  const void* k_weight;
+  float eps;
+  const int32_t* positions;
+  int rotate, rotate_keys;
+  void* q_out;
+  void* k_out;
+  void* v_out;
+  unsigned long long turn[64];  // rotation pair i: frac(theta_i / 2 pi) * 2^64, as DecodeParams::rope_turn
+};
+
+struct VerifyParams {
+  const float* target;
+  const float* draft;  // or NULL
+  long long tstride, dstride;
+  int V, N, batch;
+  const int32_t* tokens;
+  const int32_t* parents;
+  const float* uniforms;
+  int32_t* path;
+  int32_t* n_accepted;
+  int32_t* next_token;
   uint32_t* status;
 };
 
@@ -143,6 +207,17 @@ cudaError_t occupancy_decode_int4(int ngv, int g, int multi, int smem, int* n);
 cudaError_t occupancy_decode_int8(int ngv, int g, int multi, int smem, int* n);
 cudaError_t occupancy_decode_fp8(int ngv, int g, int multi, int smem, int* n);
 cudaError_t occupancy_decode_fp8_e5m2(int ngv, int g, int multi, int smem, int* n);
+
+// column halves of `sub` (16, 32 or 64) query columns, `ctas` CTAs, `smem` bytes
+size_t tree_fixed_smem(int sub, int batch);
+cudaError_t launch_tree_int2(const TreeParams& p, int sub, int ctas, int smem, cudaStream_t s);
+cudaError_t launch_tree_int4(const TreeParams& p, int sub, int ctas, int smem, cudaStream_t s);
+cudaError_t launch_tree_int8(const TreeParams& p, int sub, int ctas, int smem, cudaStream_t s);
+cudaError_t launch_tree_fp8(const TreeParams& p, int sub, int ctas, int smem, cudaStream_t s);
+cudaError_t launch_tree_fp8_e5m2(const TreeParams& p, int sub, int ctas, int smem, cudaStream_t s);
+
+cudaError_t launch_norm_rope(const NormRopeParams& p, cudaStream_t stream);
+cudaError_t launch_verify(const VerifyParams& p, cudaStream_t stream);
 
 cudaError_t launch_append(const AppendParams& p, cudaStream_t stream);
 cudaError_t launch_lse_merge(const float* o_parts, const float* lse_parts, int n_parts, long long rows, void* out,

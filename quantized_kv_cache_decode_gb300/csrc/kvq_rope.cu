@@ -1,0 +1,129 @@
+// Queries and keys of a fused projection, normed per head and rotated to their
+// positions, keys and values laid out for the cache's append (sm_103a).
+//
+// "KV Cache Quantization Analysis", section 3 (Keys and RoPE): channel pair
+// (i, i + 64) of a head is turned by t * base^(-2i/128) at position t.  Section 5:
+// K and V go to the cache right after they are computed.
+//   y = w x / sqrt(mean(x^2) + eps),  y'_i = y_i cos - y_{i+64} sin,  y'_{i+64} = y_{i+64} cos + y_i sin
+//
+// Bound by memory: every head is 256 bytes in and 256 bytes out.  Eight lanes hold a head,
+// two 16-byte pieces each (channels 8j.. and 64 + 8j..: both halves of its eight pairs), so
+// the sum of squares is three shuffles and the rotation none; a warp takes four heads at a
+// time.  The eight angles of a lane serve all heads of a token that its warp takes.
+#include "kvq_common.cuh"
+
+namespace kvq {
+
+constexpr int kRopeWarps = 8;
+
+__device__ __forceinline__ void bf16x8_to_f32(const uint4& v, float (&x)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = unpack_bf16(w[i]);
+    x[2 * i] = f.x;
+    x[2 * i + 1] = f.y;
+  }
+}
+__device__ __forceinline__ uint4 f32_to_bf16x8(const float (&x)[8]) {
+  return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+}
+
+// A warp takes `per` groups of four heads of one token, `parts` warps a token.
+__global__ void __launch_bounds__(32 * kRopeWarps) norm_rope_kernel(const __grid_constant__ NormRopeParams p, int per,
+                                                                    int parts) {
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31, j = lane & 7, sub = lane >> 3;
+  const long long task = (long long)blockIdx.x * kRopeWarps + (threadIdx.x >> 5);
+  const long long row = task / parts;
+  if (row >= p.rows) return;
+  const int part = (int)(task - row * parts);
+  const int heads = p.Hq + 2 * p.H, rotated = p.rotate_keys ? p.Hq + p.H : p.Hq;
+  const int h0 = part * per * 4;
+  const long long b = row / p.n_tokens;
+  const int t = (int)(row - b * p.n_tokens);
+  float cs[8], sn[8];
+  if (p.rotate && h0 < rotated) {
+    // the angle in turns is position * turn mod 1, in 64-bit fixed point: its top 32 bits, signed,
+    // are the angle in units of 2^-31 half turns
+    const unsigned long long pos = (unsigned long long)(long long)p.positions[row];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int top = (int)(uint32_t)((pos * p.turn[8 * j + i]) >> 32);
+      sincospif((float)top * 4.656612873077393e-10f, &sn[i], &cs[i]);
+    }
+  }
+  float wq[16], wk[16];
+  const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.qkv) + row * p.row_stride);
+  for (int g = 0; g < per; ++g) {
+    const int h = h0 + 4 * g + sub;
+    const bool on = h < heads;
+    uint4 a = make_uint4(0, 0, 0, 0), c = a;
+    if (on) {
+      a = src[h * 16 + j];
+      c = src[h * 16 + 8 + j];
+    }
+    const bool isq = h < p.Hq, isk = !isq && h < p.Hq + p.H;
+    const uint4* w = reinterpret_cast<const uint4*>(isq ? p.q_weight : p.k_weight);
+    float x[8], y[8];
+    bf16x8_to_f32(a, x);
+    bf16x8_to_f32(c, y);
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], fmaf(y[i], y[i], ss));
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    if (!on) continue;
+    if (isq || isk) {
+      if (w) {
+        const float r = 1.0f / sqrtf(ss * (1.0f / 128.0f) + p.eps);
+        float u[8], v[8];
+        bf16x8_to_f32(w[j], u);
+        bf16x8_to_f32(w[8 + j], v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          x[i] = x[i] * r * u[i];
+          y[i] = y[i] * r * v[i];
+        }
+      }
+      if (p.rotate && h < rotated) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float xi = x[i];
+          x[i] = xi * cs[i] - y[i] * sn[i];
+          y[i] = y[i] * cs[i] + xi * sn[i];
+        }
+      }
+      a = f32_to_bf16x8(x);
+      c = f32_to_bf16x8(y);
+    }
+    uint4* dst;
+    if (isq) {
+      dst = reinterpret_cast<uint4*>(p.q_out) + (row * p.Hq + h) * 16;
+    } else {
+      const int hk = isk ? h - p.Hq : h - p.Hq - p.H;
+      dst = reinterpret_cast<uint4*>(isk ? p.k_out : p.v_out) + ((b * p.H + hk) * p.n_tokens + t) * 16;
+    }
+    dst[j] = a;
+    dst[8 + j] = c;
+  }
+}
+
+cudaError_t launch_norm_rope(const NormRopeParams& p, cudaStream_t stream) {
+  const int groups = (p.Hq + 2 * p.H + 3) / 4;
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  // few tokens: a warp per four heads, so that all SMs take part; many: more heads per warp share the angles
+  int parts = groups;
+  while (parts > 1 && p.rows * (parts / 2) >= 32LL * sms) parts /= 2;
+  const int per = (groups + parts - 1) / parts;
+  parts = (groups + per - 1) / per;
+  const long long blocks = (p.rows * parts + kRopeWarps - 1) / kRopeWarps;
+  if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
+  return launch_pdl(norm_rope_kernel, dim3((unsigned)blocks), dim3(32 * kRopeWarps), 0, stream, p, per, parts);
+}
+
+}  // namespace kvq

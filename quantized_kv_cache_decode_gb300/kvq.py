@@ -29,6 +29,7 @@ KVQ_OK = 0
 STATUS = {0: "KVQ_OK", -1: "KVQ_ERR_INVALID_ARG", -2: "KVQ_ERR_UNSUPPORTED", -3: "KVQ_ERR_CUDA",
           -4: "KVQ_ERR_WORKSPACE"}
 DEV_BAD_BLOCK, DEV_CAPACITY, DEV_TIMEOUT = 0x1, 0x2, 0x4
+DEV_BAD_TREE, DEV_RANGE, DEV_BAD_PROBS = 0x8, 0x10, 0x20
 FORMATS = {"bf16": 1, "int2": 2, "int4": 4, "int8": 8, "fp8_e4m3": 16, "fp8_e5m2": 17}
 FP8_FORMATS = (FORMATS["fp8_e4m3"], FORMATS["fp8_e5m2"])
 FIELDS = ["qstore", "block_pool", "resid_k", "resid_v", "sink_k", "sink_v"]
@@ -74,6 +75,15 @@ _lib.kvq_decode_combine.argtypes = [_P(LayerConfig), c_i32, c_i32, c_vp, c_i32, 
 _lib.kvq_decode_attention_static_scratch.argtypes = [_P(LayerConfig), _P(LayerCache), c_vp, c_i32, c_vp, c_i32,
                                                      ctypes.c_float, c_vp, c_i32, c_vp, c_vp, c_vp]
 _lib.kvq_dequantize.argtypes = [_P(LayerConfig), _P(LayerCache), c_vp, c_i32, c_i32, c_vp, c_vp, c_vp, c_vp]
+_lib.kvq_qk_norm_rope.argtypes = [c_vp, ctypes.c_int64, c_i32, c_i32, c_i32, c_i32, c_i32, c_vp, c_vp, ctypes.c_float,
+                                  c_vp, ctypes.c_float, c_i32, c_vp, c_vp, c_vp, c_vp]
+_lib.kvq_decode_attention_tree.argtypes = [_P(LayerConfig), _P(LayerCache), c_vp, c_vp, c_vp, c_vp, c_i32, c_i32, c_vp,
+                                           c_i32, ctypes.c_float, c_vp, c_i32, c_vp, c_vp, c_sz, c_vp, c_vp]
+_lib.kvq_decode_workspace_size_tree.argtypes = [_P(LayerConfig), c_i32, c_i32, c_i32, _P(c_sz)]
+_lib.kvq_verify_tree.argtypes = [c_vp, ctypes.c_int64, c_vp, ctypes.c_int64, c_i32, c_vp, c_vp, c_vp, c_i32, c_i32,
+                                 c_vp, c_vp, c_vp, c_vp, c_vp]
+_lib.kvq_append_accepted.argtypes = [_P(LayerConfig), _P(LayerCache), c_vp, c_vp, c_i32, c_vp, c_vp, c_vp, c_i32, c_vp,
+                                     c_vp]
 _lib.kvq_status_string.argtypes = [c_i32]
 _lib.kvq_status_string.restype = ctypes.c_char_p
 for _fn in ("kvq_cache_layout", "kvq_fp8_calibrate", "kvq_fp8_calibrate_format", "kvq_quantize_append",
@@ -81,7 +91,9 @@ for _fn in ("kvq_cache_layout", "kvq_fp8_calibrate", "kvq_fp8_calibrate_format",
             "kvq_decode_attention", "kvq_decode_partials", "kvq_decode_combine", "kvq_dequantize",
             "kvq_decode_attention_multi", "kvq_decode_workspace_size_multi", "kvq_lse_merge",
             "kvq_selftest_bounded_wait",
-            "kvq_decode_attention_static_scratch", "kvq_append_decode_attention"):
+            "kvq_decode_attention_static_scratch", "kvq_append_decode_attention",
+            "kvq_qk_norm_rope", "kvq_decode_attention_tree", "kvq_decode_workspace_size_tree", "kvq_verify_tree",
+            "kvq_append_accepted"):
     getattr(_lib, _fn).restype = c_i32
 
 
@@ -244,6 +256,54 @@ def dequantize(cfg: LayerConfig, cache: LayerCache, seq_lens, batch: int, max_to
     _check("kvq_dequantize",
            _lib.kvq_dequantize(ctypes.byref(cfg), ctypes.byref(cache), _ptr(seq_lens), batch, max_tokens,
                                _ptr(k_out), _ptr(v_out), _ptr(dev_status), _stream_ptr(stream)))
+
+
+def qk_norm_rope(qkv, row_stride: int, batch: int, n_tokens: int, num_q_heads: int, num_kv_heads: int, q_weight,
+                 k_weight, eps: float, positions, rope_base: float, rotate_keys: bool, q_out, k_out, v_out,
+                 head_dim: int = 128, stream=None) -> None:
+    """Per-head norm and rotation of a fused projection's queries and keys; keys and values in the append's layout."""
+    _check("kvq_qk_norm_rope",
+           _lib.kvq_qk_norm_rope(_ptr(qkv), row_stride, batch, n_tokens, num_q_heads, num_kv_heads, head_dim,
+                                 _ptr(q_weight), _ptr(k_weight), eps, _ptr(positions), rope_base, int(rotate_keys),
+                                 _ptr(q_out), _ptr(k_out), _ptr(v_out), _stream_ptr(stream)))
+
+
+def decode_workspace_size_tree(cfg: LayerConfig, batch: int, n_nodes: int, num_q_heads: int) -> int:
+    """Workspace bytes of decode_attention_tree (kvq_decode_workspace_size_tree)."""
+    out = c_sz(0)
+    _check("kvq_decode_workspace_size_tree",
+           _lib.kvq_decode_workspace_size_tree(ctypes.byref(cfg), batch, n_nodes, num_q_heads, ctypes.byref(out)))
+    return int(out.value)
+
+
+def decode_attention_tree(cfg: LayerConfig, cache: LayerCache, q, k_draft, v_draft, parents, n_nodes: int,
+                          num_q_heads: int, seq_lens, batch: int, softmax_scale: float, out, out_bf16: bool, lse,
+                          workspace, workspace_bytes: int, dev_status=None, stream=None) -> None:
+    """Attention of a drafted tree's nodes over the cache and their ancestors; q, out: [B][n_nodes][Hq][d]."""
+    _check("kvq_decode_attention_tree",
+           _lib.kvq_decode_attention_tree(ctypes.byref(cfg), ctypes.byref(cache), _ptr(q), _ptr(k_draft),
+                                          _ptr(v_draft), _ptr(parents), n_nodes, num_q_heads, _ptr(seq_lens), batch,
+                                          softmax_scale, _ptr(out), int(out_bf16), _ptr(lse), _ptr(workspace),
+                                          workspace_bytes, _ptr(dev_status), _stream_ptr(stream)))
+
+
+def verify_tree(target_probs, target_stride: int, draft_probs, draft_stride: int, vocab: int, tokens, parents,
+                uniforms, n_nodes: int, batch: int, path, n_accepted, next_token, dev_status=None,
+                stream=None) -> None:
+    """Accepted path and next token of drafted trees; draft_probs None: the nodes were chosen, not drawn."""
+    _check("kvq_verify_tree",
+           _lib.kvq_verify_tree(_ptr(target_probs), target_stride, _ptr(draft_probs), draft_stride, vocab,
+                                _ptr(tokens), _ptr(parents), _ptr(uniforms), n_nodes, batch, _ptr(path),
+                                _ptr(n_accepted), _ptr(next_token), _ptr(dev_status), _stream_ptr(stream)))
+
+
+def append_accepted(cfg: LayerConfig, cache: LayerCache, k_draft, v_draft, n_nodes: int, path, n_accepted, seq_lens,
+                    batch: int, dev_status=None, stream=None) -> None:
+    """Append rows path[b][:n_accepted[b]] of the drafted keys and values to every sequence."""
+    _check("kvq_append_accepted",
+           _lib.kvq_append_accepted(ctypes.byref(cfg), ctypes.byref(cache), _ptr(k_draft), _ptr(v_draft), n_nodes,
+                                    _ptr(path), _ptr(n_accepted), _ptr(seq_lens), batch, _ptr(dev_status),
+                                    _stream_ptr(stream)))
 
 
 # --------------------------------------------------------------------------- #
