@@ -756,20 +756,30 @@ kvq_status kvq_verify_tree(const float* target_probs, int64_t target_stride, con
 namespace kvq {
 namespace {
 
+// Largest token count that a sequence of the layer can hold (max_tokens of the kernels).
+long long max_seq_tokens(const LayerDesc& L) {
+  if (L.bf16) return (long long)L.S + L.W;
+  const long long q = L.paged ? (long long)L.mbps * L.P : (long long)L.cap;
+  return L.fp8 ? L.S + q : L.S + q + L.R + L.G - 1;
+}
+
 struct TreeGeom {
-  int sub, chunks, ctas, smem, nslots, slot_bytes, slot_hdr, bf_tokens;
+  int nt, chunks, ctas, smem, nslots, slot_bytes, slot_hdr, bf_tokens;
   size_t off_ml, off_counters, ws_bytes;
 };
 
-// Launch shape of the tree attention: the narrowest column halves that hold all columns in one
-// chunk (64-column halves and several chunks beyond 128), one CTA per SM, as many slots as fit.
+// Launch shape of the tree attention: the fewest columns a CTA that hold all in one chunk
+// (several chunks beyond 128), one CTA per SM, as many slots as fit.
 kvq_status tree_geometry(const LayerDesc& L, int batch, int columns, TreeGeom* G) {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return KVQ_ERR_CUDA;
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return KVQ_ERR_CUDA;
-  G->sub = columns <= 32 ? 16 : (columns <= 64 ? 32 : 64);
-  G->chunks = (columns + 2 * G->sub - 1) / (2 * G->sub);
+  G->nt = columns <= 32 ? 32 : (columns <= 64 ? 64 : 128);
+  G->chunks = (columns + G->nt - 1) / G->nt;
   G->ctas = sms;
+  // the kernel counts the launch's blocks of 128 tokens in 32 bits
+  const long long most = (max_seq_tokens(L) + kMaxNodes) / 128 + 2;
+  if (most * batch > 0x7FFFFFFFLL / ((long long)L.H * G->chunks)) return KVQ_ERR_UNSUPPORTED;
   // a quantized slot: 64 tokens, the headers of the records that they touch first
   int headers = 0;
   if (!L.fp8 && !L.bf16) headers = L.tpg == 1 ? 4 : (L.tpg % 4 == 0 ? 1 : 2);
@@ -777,12 +787,12 @@ kvq_status tree_geometry(const LayerDesc& L, int batch, int columns, TreeGeom* G
   const int need = L.bf16 ? 0 : G->slot_hdr + 4 * L.tile_bytes;
   G->slot_bytes = (std::max(need, L.bf16 ? 32768 : 16384) + 127) / 128 * 128;
   G->bf_tokens = G->slot_bytes >= 32768 ? 64 : 32;
-  const size_t fixed = tree_fixed_smem(G->sub, batch);
+  const size_t fixed = tree_fixed_smem(G->nt, batch);
   const size_t budget = 227 * 1024;
   if (fixed + 2 * (size_t)G->slot_bytes > budget) return KVQ_ERR_UNSUPPORTED;
   G->nslots = (int)std::min<size_t>(12, (budget - fixed) / G->slot_bytes);
   G->smem = (int)(fixed + (size_t)G->nslots * G->slot_bytes);
-  const size_t rows = 2 * (size_t)G->ctas * 2 * G->sub;
+  const size_t rows = 2 * (size_t)G->ctas * G->nt;
   G->off_ml = rows * kHeadDim * sizeof(float);
   G->off_counters = G->off_ml + rows * 2 * sizeof(float);
   G->ws_bytes = G->off_counters + (size_t)batch * L.H * G->chunks * sizeof(unsigned);
@@ -795,6 +805,7 @@ kvq_status check_tree_args(const kvq_layer_config* cfg, int32_t n_nodes, int32_t
   if (st != KVQ_OK) return st;
   if (n_nodes < 1 || n_nodes > kMaxNodes) return KVQ_ERR_INVALID_ARG;
   if (L->rope || L->k_out || L->v_out) return KVQ_ERR_UNSUPPORTED;
+  if ((long long)batch * n_nodes * num_q_heads > 0x7FFFFFFFLL) return KVQ_ERR_UNSUPPORTED;  // (rows counted in 32 bits)
   return KVQ_OK;
 }
 
@@ -861,11 +872,11 @@ kvq_status kvq_decode_attention_tree(const kvq_layer_config* cfg, const kvq_laye
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   switch (kernel_format(L.fmt)) {
-    case KVQ_FMT_INT2: e = launch_tree_int2(p, G.sub, G.ctas, G.smem, s); break;
-    case KVQ_FMT_INT4: e = launch_tree_int4(p, G.sub, G.ctas, G.smem, s); break;
-    case KVQ_FMT_INT8: e = launch_tree_int8(p, G.sub, G.ctas, G.smem, s); break;
-    case KVQ_FMT_FP8_E5M2: e = launch_tree_fp8_e5m2(p, G.sub, G.ctas, G.smem, s); break;
-    default: e = launch_tree_fp8(p, G.sub, G.ctas, G.smem, s); break;
+    case KVQ_FMT_INT2: e = launch_tree_int2(p, G.nt, G.ctas, G.smem, s); break;
+    case KVQ_FMT_INT4: e = launch_tree_int4(p, G.nt, G.ctas, G.smem, s); break;
+    case KVQ_FMT_INT8: e = launch_tree_int8(p, G.nt, G.ctas, G.smem, s); break;
+    case KVQ_FMT_FP8_E5M2: e = launch_tree_fp8_e5m2(p, G.nt, G.ctas, G.smem, s); break;
+    default: e = launch_tree_fp8(p, G.nt, G.ctas, G.smem, s); break;
   }
   return e == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
 }

@@ -116,13 +116,13 @@ struct TreeParams {
   const int32_t* parents;  // [B][N]
   const int32_t* seq_lens;
   int N, Hq, gh, batch;
-  int chunks;      // column chunks of 2 * SUB per (sequence, kv head)
+  int chunks;      // column chunks of NT per (sequence, kv head)
   int nslots, slot_bytes;
   int slot_hdr;    // bytes of record headers at the start of a quantized slot
   int bf_tokens;   // bf16 tokens per slot (K rows, then V rows)
   float scale_log2;
-  float* ws_o;     // [2 per CTA][2 * SUB][d] unnormalised partial outputs
-  float* ws_ml;    // [2 per CTA][2 * SUB][2] maximum (log2 domain) and sum
+  float* ws_o;     // [2 per CTA][NT][d] unnormalised partial outputs
+  float* ws_ml;    // [2 per CTA][NT][2] maximum (log2 domain) and sum
   unsigned* counters;  // [B * H * chunks], zero between calls
   uint32_t* status;
   void* out;
@@ -208,13 +208,13 @@ cudaError_t occupancy_decode_int8(int ngv, int g, int multi, int smem, int* n);
 cudaError_t occupancy_decode_fp8(int ngv, int g, int multi, int smem, int* n);
 cudaError_t occupancy_decode_fp8_e5m2(int ngv, int g, int multi, int smem, int* n);
 
-// column halves of `sub` (16, 32 or 64) query columns, `ctas` CTAs, `smem` bytes
-size_t tree_fixed_smem(int sub, int batch);
-cudaError_t launch_tree_int2(const TreeParams& p, int sub, int ctas, int smem, cudaStream_t s);
-cudaError_t launch_tree_int4(const TreeParams& p, int sub, int ctas, int smem, cudaStream_t s);
-cudaError_t launch_tree_int8(const TreeParams& p, int sub, int ctas, int smem, cudaStream_t s);
-cudaError_t launch_tree_fp8(const TreeParams& p, int sub, int ctas, int smem, cudaStream_t s);
-cudaError_t launch_tree_fp8_e5m2(const TreeParams& p, int sub, int ctas, int smem, cudaStream_t s);
+// `nt` (32, 64 or 128) query columns a CTA, `ctas` CTAs, `smem` bytes
+size_t tree_fixed_smem(int nt, int batch);
+cudaError_t launch_tree_int2(const TreeParams& p, int nt, int ctas, int smem, cudaStream_t s);
+cudaError_t launch_tree_int4(const TreeParams& p, int nt, int ctas, int smem, cudaStream_t s);
+cudaError_t launch_tree_int8(const TreeParams& p, int nt, int ctas, int smem, cudaStream_t s);
+cudaError_t launch_tree_fp8(const TreeParams& p, int nt, int ctas, int smem, cudaStream_t s);
+cudaError_t launch_tree_fp8_e5m2(const TreeParams& p, int nt, int ctas, int smem, cudaStream_t s);
 
 cudaError_t launch_norm_rope(const NormRopeParams& p, cudaStream_t stream);
 cudaError_t launch_verify(const VerifyParams& p, cudaStream_t stream);

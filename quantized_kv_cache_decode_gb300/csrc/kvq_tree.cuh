@@ -16,12 +16,12 @@
 // operand fragment, which is also what tcgen05.st's 16x128b shape takes: dequantized
 // fragments go straight from registers to tensor memory.
 //
-// A CTA works on 128 cache tokens at a time ("block") and at most 2 * SUB columns, in
-// two halves of SUB columns whose score, softmax and output steps alternate:
+// A CTA works on 128 cache tokens ("block") and NT = 32, 64 or 128 columns at a time:
 //   loader warp     cache bytes -> shared-memory slots (bulk copies; bf16 rows: cp.async)
-//   dequant warps   slots -> K, V^T as f16 in tensor memory (two buffers each)
-//   one MMA thread  the tcgen05.mma of both products
-//   softmax warps   scores -> P (one warpgroup per half), running maximum and sum in fp32
+//   dequant warps   slots -> K and V^T as f16 in tensor memory, a warpgroup for each
+//   MMA warp        the tcgen05.mma of both products (scores of the next block before the outputs of this one)
+//   softmax warps   scores -> P (a warpgroup per half of the columns), running maximum and sum in fp32
+//   check warp      (integer layers) the scales of every slot: does f16 hold what they stand for
 // The blocks of all (sequence, kv head, column chunk) items are divided evenly over one
 // CTA per SM; an item cut between CTAs is merged by the last CTA to finish it, in CTA
 // order (the result does not depend on which one that is).
@@ -74,6 +74,11 @@ __device__ __forceinline__ void tc_st_frag4(uint32_t taddr, const uint32_t (&r)[
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
+__device__ __forceinline__ void tc_st_frag2(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
 // 32 lanes x 16 columns, one lane per thread
 __device__ __forceinline__ void tc_ld16(uint32_t taddr, float* x) {
   uint32_t* u = reinterpret_cast<uint32_t*>(x);
@@ -112,6 +117,20 @@ __device__ __forceinline__ float exp2_approx(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ float2 add_f32x2(float2 a, float2 b) {
+  float2 d;
+  asm("{ .reg .b64 ra, rb, rd; mov.b64 ra, {%2, %3}; mov.b64 rb, {%4, %5}; add.rn.f32x2 rd, ra, rb; "
+      "mov.b64 {%0, %1}, rd; }"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+// one lane of the warp
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(r));
+  return r != 0;
+}
 // v f; a sum that is still 0 stays so whatever f is
 __device__ __forceinline__ float scaled(float v, float f) { return v == 0.f ? 0.f : v * f; }
 __device__ __forceinline__ void named_sync(int id, int threads) {
@@ -132,50 +151,63 @@ __device__ __forceinline__ bool named_any(int id, int threads, bool v) {
 // ---------------------------------------------------------------------------
 constexpr int kBlk = 128;  // cache tokens per block
 
-template <int SUB>
+template <int NT>
 struct TreeShape {
-  // 64-column halves are bound by the softmax warps and need their registers; narrower ones by
-  // the dequantization, which then gets a warpgroup for K and one for V
-  static constexpr int kDq = SUB == 64 ? 4 : 8;
-  static constexpr int kWarps = kDq + 8 + 4;  // (the last warpgroup: MMA, loader, two idle)
+  static constexpr int kSub = NT / 2;              // columns of a softmax warpgroup
+  static constexpr int kWarps = 20;                // 4 K, 4 V, 8 softmax, then loader, MMA, check, (idle)
   static constexpr int kThreads = 32 * kWarps;
   // registers a thread: at launch, then by role (the roles' warpgroups together stay within the launch's)
-  static constexpr int kRegLaunch = SUB == 64 ? 128 : 96;
-  static constexpr int kRegDq = SUB == 64 ? 112 : 88, kRegSm = SUB == 64 ? 168 : 112, kRegIo = 64;
-  static_assert(kDq / 4 * kRegDq + 2 * kRegSm + kRegIo <= (kWarps / 4) * kRegLaunch, "register split");
-  static constexpr int kQBytes = SUB * 256;        // one half's queries (f16, two 64-channel halves)
-  static constexpr int kPBytes = kBlk * SUB * 2;   // one half's P (f16, token rows)
-  static constexpr int kFixed = 2 * kQBytes + 2 * kPBytes;
+  static constexpr int kRegLaunch = 96;
+  static constexpr int kRegDq = NT == 128 ? 80 : 88, kRegSm = NT == 128 ? 136 : 128, kRegIo = 48;
+  static_assert(2 * kRegDq + 2 * kRegSm + kRegIo <= 5 * kRegLaunch, "register split");
+  static constexpr int kQBytes = NT * 256;         // queries (f16): [two 64-channel halves][NT rows of 128 bytes]
+  static constexpr int kPBytes = kBlk * NT * 2;    // one buffer of P (f16)
+  static constexpr int kFixed = kQBytes + 2 * kPBytes;
+  // tensor memory: scores and outputs take NT columns each (scores twice), K and V 64 each, twice where there is room
+  static constexpr int kKv = NT == 128 ? 1 : 2;
+  static constexpr uint32_t kTmK = 0, kTmV = 64 * kKv, kTmS = 128 * kKv, kTmO = 128 * kKv + 2 * NT;
+  static_assert(kTmO + NT <= 512, "tensor memory");
+  // P rows (one per token): NT <= 64 columns in one row of 2 NT bytes, 128 as two 64-column regions, in the
+  // swizzle of that row length (B operand with the columns contiguous)
+  static constexpr int kPRow = NT == 32 ? 64 : 128;
+  static constexpr uint32_t kPSwizzle = NT == 32 ? 4 : 2, kPMask = NT == 32 ? 3 : 7;
 };
-
-// tensor-memory columns
-constexpr uint32_t kTmK = 0, kTmV = 128, kTmS = 256, kTmO = 384;
 
 constexpr int kMaxSlots = 12;
 constexpr long long kTreeWait = kWaitLimitCycles;
 
+// One cut of an item: blocks [blk0, blk1) of (sequence b, kv head h, column chunk ch)
+struct TreeSeg {
+  int b, h, ch, blk0, blk1, nblk, nq;
+  int n_sink, qn, r;  // the sequence's tokens: sink, quantized, window
+  unsigned item0;     // first unit of the item
+};
+
+// A warp's position in its CTA's units
+struct TreeCursor {
+  unsigned u, end;
+  int b;
+};
+
 struct TreeSmem {  // small shared state, after the big buffers
   unsigned long long slot_full[kMaxSlots], slot_empty[kMaxSlots];
   unsigned long long k_full[2], k_empty[2], v_full[2], v_empty[2];
-  unsigned long long s_full[2], s_free[2], p_full[2], p_free[2], q_full[2], drain;
+  unsigned long long s_full[2], s_free[2], p_full[2], p_free[2], q_full, drain;
   uint32_t slot_ok[kMaxSlots];  // quantized slots: which of the four tiles were copied
   uint32_t tmem;
   int abort;
-  int last;      // merge: this CTA finished the item
-  alignas(16) float m[2][64];   // running maximum of each column (log2 domain; 0 until one is set)
-  alignas(16) float red[2][4][64];
-  alignas(16) float rise[2][64], fall[2][64];  // change of the maxima and what it scales sums by
+  int last;                       // merge: this CTA finished the item
+  alignas(16) float m[128];       // running maximum of each column (log2 domain; 0 until one is set)
+  alignas(16) float fall[128];    // what a change of the maxima scales sums by; epilogue: 1 / sum
+  alignas(16) float red[4][128];  // the four warps' maxima or sums
+  int row[128];                   // epilogue: the columns' rows of the output, -1: none
   int unset[2];
-  unsigned long long anc[2][64];  // a node's ancestors and itself
-  unsigned long long wild[2];     // nodes whose drafted Values f16 does not hold
-  int par[2][64];
-};
-
-// One cut of an item: blocks [blk0, blk1) of (sequence b, kv head h, column chunk ch)
-struct TreeSeg {
-  int b, h, ch, blk0, blk1, nblk, nq, T;
-  long long item0;  // first unit of the item
-  TokenSplit ts;
+  unsigned long long anc[64];     // a node's ancestors and itself
+  unsigned long long wild;        // nodes whose drafted Values f16 does not hold
+  int par[64];
+  unsigned units, ctas;           // blocks of the launch, CTAs that share them
+  TreeCursor cur[20];             // per warp
+  TreeSeg seg[20];
 };
 
 // node n's ancestors and itself; par[n] < n, or -1
@@ -185,46 +217,54 @@ __device__ __forceinline__ unsigned long long tree_ancestors(const int* par, int
   return a;
 }
 
-struct TreeCursor {
-  long long u, end;
-  int b;
-};
-
-__device__ __forceinline__ TreeCursor tree_cursor(const TreeParams& p, const int* pre, long long lo, long long hi) {
-  TreeCursor c;
+__device__ __forceinline__ void tree_cursor(const TreeParams& p, const int* pre, unsigned lo, unsigned hi, TreeCursor& c) {
   c.u = lo;
   c.end = hi;
   int a = 0, z = p.batch - 1;  // the last sequence whose first unit is <= lo
-  const long long hc = (long long)p.L.H * p.chunks;
+  const unsigned hc = (unsigned)(p.L.H * p.chunks);
   while (a < z) {
     const int m = (a + z + 1) >> 1;
-    if ((long long)pre[m] * hc <= lo) a = m;
+    if ((unsigned)pre[m] * hc <= lo) a = m;
     else z = m - 1;
   }
   c.b = a;
-  return c;
 }
 
+// First unit of CTA c of W
+__device__ __forceinline__ unsigned tree_unit(unsigned U, unsigned W, unsigned c) {
+  return (unsigned)((unsigned long long)U * c / W);
+}
+
+// The warp's next cut, in shared memory (roles keep few of its fields in registers); false behind the last.
 __device__ __forceinline__ bool tree_next(const TreeParams& p, const int* pre, const int* lens, TreeCursor& c,
                                           TreeSeg& s) {
-  if (c.u >= c.end) return false;
-  const long long hc = (long long)p.L.H * p.chunks;
-  while (c.b + 1 < p.batch && (long long)pre[c.b + 1] * hc <= c.u) ++c.b;
-  s.b = c.b;
-  s.nblk = pre[c.b + 1] - pre[c.b];
-  const long long off = c.u - (long long)pre[c.b] * hc;
-  const long long item = off / s.nblk;
-  s.blk0 = (int)(off - item * s.nblk);
-  s.h = (int)(item / p.chunks);
-  s.ch = (int)(item - (long long)s.h * p.chunks);
-  const long long left = c.end - c.u;
-  s.blk1 = left < s.nblk - s.blk0 ? s.blk0 + (int)left : s.nblk;
-  s.item0 = c.u - s.blk0;
-  s.T = lens[c.b];
-  s.ts = split_tokens(s.T, p.L);
-  s.nq = (s.ts.qn + kBlk - 1) / kBlk;
-  c.u += s.blk1 - s.blk0;
-  return true;
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0 && c.u < c.end) {
+    const unsigned hc = (unsigned)(p.L.H * p.chunks);
+    int b = c.b;
+    while (b + 1 < p.batch && (unsigned)pre[b + 1] * hc <= c.u) ++b;
+    c.b = b;
+    const unsigned nblk = (unsigned)(pre[b + 1] - pre[b]);
+    const unsigned off = c.u - (unsigned)pre[b] * hc, item = off / nblk, blk0 = off - item * nblk;
+    const unsigned left = c.end - c.u, n = left < nblk - blk0 ? left : nblk - blk0;
+    const TokenSplit ts = split_tokens(lens[b], p.L);
+    s.b = b;
+    s.h = (int)(item / (unsigned)p.chunks);
+    s.ch = (int)(item % (unsigned)p.chunks);
+    s.blk0 = (int)blk0;
+    s.blk1 = (int)(blk0 + n);
+    s.nblk = (int)nblk;
+    s.nq = (ts.qn + kBlk - 1) / kBlk;
+    s.n_sink = ts.n_sink;
+    s.qn = ts.qn;
+    s.r = ts.r;
+    s.item0 = c.u - blk0;
+    c.u += n;
+  } else if ((threadIdx.x & 31) == 0) {
+    s.blk1 = -1;
+  }
+  __syncwarp();
+  return *const_cast<volatile int*>(&s.blk1) >= 0;
 }
 
 // Wait for a barrier phase; false when the bound ran out here or elsewhere in the CTA.
@@ -345,6 +385,36 @@ __device__ __forceinline__ void load_words(const uint8_t* codes, int lane, uint3
   }
 }
 
+// scales s and -s z of a tile's Values, group j, for the tokens 2q, 2q + 1, 2q + 8, 2q + 9
+__device__ __forceinline__ void value_scales(const float* vs, int ngv, int j, int q, float4& sc, float4& nz) {
+  const float* vz = vs + 16 * ngv;
+  float4 z;
+  if (ngv == 1) {
+    const float2 a = *reinterpret_cast<const float2*>(vs + 2 * q), b = *reinterpret_cast<const float2*>(vs + 2 * q + 8);
+    const float2 c = *reinterpret_cast<const float2*>(vz + 2 * q), d = *reinterpret_cast<const float2*>(vz + 2 * q + 8);
+    sc = make_float4(a.x, a.y, b.x, b.y);
+    z = make_float4(c.x, c.y, d.x, d.y);
+  } else {
+    const int i0 = 2 * q * ngv + j, i1 = i0 + ngv, i2 = i0 + 8 * ngv, i3 = i2 + ngv;
+    sc = make_float4(vs[i0], vs[i1], vs[i2], vs[i3]);
+    z = make_float4(vz[i0], vz[i1], vz[i2], vz[i3]);
+  }
+  nz = make_float4(-sc.x * z.x, -sc.y * z.y, -sc.z * z.z, -sc.w * z.w);
+}
+// largest magnitude that a group of scale s and zero point z stands for
+__device__ __forceinline__ float group_reach(float s, float z, float levels) {
+  return fabsf(s) * fmaxf(fabsf(z), fabsf(levels - z));
+}
+// f16 pair of tokens t, t + 1: all ones where the token is below n
+__device__ __forceinline__ uint32_t pair_mask(int t, int n) {
+  return (t < n ? 0xFFFFu : 0u) | (t + 1 < n ? 0xFFFF0000u : 0u);
+}
+__device__ __forceinline__ void put_out(const TreeParams& p, int row, int c, float v) {
+  const long long at = (long long)row * 128 + c;
+  if (p.out_bf16) reinterpret_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(v);
+  else reinterpret_cast<float*>(p.out)[at] = v;
+}
+
 // bf16 rows in a slot: token row of 256 bytes, its 16-byte chunks permuted so that the
 // operand reads below are free of bank conflicts (K: 8-byte reads of 4 rows x 2 chunks;
 // V: ldmatrix over 8 rows)
@@ -364,29 +434,28 @@ __device__ __forceinline__ uint32_t abs_max2(uint32_t m, uint32_t w) { return __
 // ---------------------------------------------------------------------------
 // the kernel
 // ---------------------------------------------------------------------------
-template <int FMT, int SUB>
-__global__ void __launch_bounds__(TreeShape<SUB>::kThreads, 1) tree_kernel(const __grid_constant__ TreeParams p) {
-  using Sh = TreeShape<SUB>;
+template <int FMT, int NT>
+__global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const __grid_constant__ TreeParams p) {
+  using Sh = TreeShape<NT>;
   using F = TreeFmt<FMT>;
+  constexpr int SUB = Sh::kSub;
+  constexpr uint32_t kAll = 0xffffffffu;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   const LayerDesc& L = p.L;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  uint8_t* const Qs = smem;                      // [2 halves][SUB rows]
-  uint8_t* const Ps = smem + 2 * Sh::kQBytes;    // [2 halves][128 tokens][SUB]
+  const int tid = threadIdx.x, warp = __shfl_sync(kAll, tid >> 5, 0), lane = tid & 31;
+  uint8_t* const Qs = smem;
+  uint8_t* const Ps = smem + Sh::kQBytes;
   uint8_t* const slots = smem + Sh::kFixed;
   TreeSmem& S = *reinterpret_cast<TreeSmem*>(slots + (size_t)p.nslots * p.slot_bytes);
   int* const pre = reinterpret_cast<int*>(&S + 1);  // [batch + 1] blocks before
-  int* const lens = pre + p.batch + 1;                                               // [batch] tokens
-
-  pdl_wait();
-  pdl_trigger();
+  int* const lens = pre + p.batch + 1;              // [batch] tokens
 
   // ---- set-up: barriers, tensor memory, the batch's block counts ----
   if (tid == 0) {
     for (int i = 0; i < kMaxSlots; ++i) {
       mbar_init(smem_addr(&S.slot_full[i]), 32);
-      mbar_init(smem_addr(&S.slot_empty[i]), Sh::kDq);
+      mbar_init(smem_addr(&S.slot_empty[i]), F::kFp8 ? 8 : 9);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_addr(&S.k_full[i]), 4);
@@ -394,20 +463,22 @@ __global__ void __launch_bounds__(TreeShape<SUB>::kThreads, 1) tree_kernel(const
       mbar_init(smem_addr(&S.v_full[i]), 4);
       mbar_init(smem_addr(&S.v_empty[i]), 1);
       mbar_init(smem_addr(&S.s_full[i]), 1);
-      mbar_init(smem_addr(&S.s_free[i]), 4);
-      mbar_init(smem_addr(&S.p_full[i]), 4);
+      mbar_init(smem_addr(&S.s_free[i]), 8);
+      mbar_init(smem_addr(&S.p_full[i]), 8);
       mbar_init(smem_addr(&S.p_free[i]), 1);
-      mbar_init(smem_addr(&S.q_full[i]), 4);
     }
+    mbar_init(smem_addr(&S.q_full), 8);
     mbar_init(smem_addr(&S.drain), 1);
     S.abort = 0;
     S.unset[0] = S.unset[1] = 0;
     fence_barrier_init();
   }
-  if (warp == Sh::kDq + 8) {
+  if (warp == 17) {
     tc_alloc512(smem_addr(&S.tmem));
     tc_relinquish();
   }
+  pdl_wait();
+  pdl_trigger();
   for (int b = tid; b < p.batch; b += Sh::kThreads) {
     long long T = p.seq_lens[b];
     const long long cap = max_tokens(L);
@@ -424,299 +495,328 @@ __global__ void __launch_bounds__(TreeShape<SUB>::kThreads, 1) tree_kernel(const
   if (warp == 0) {
     int run = 0;
     if (lane == 0) pre[0] = 0;
+#pragma unroll 1
     for (int b0 = 0; b0 < p.batch; b0 += 32) {
       int v = b0 + lane < p.batch ? pre[b0 + lane + 1] : 0;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, v, o);
+        const int x = __shfl_up_sync(kAll, v, o);
         if (lane >= o) v += x;
       }
       if (b0 + lane < p.batch) pre[b0 + lane + 1] = run + v;
-      run += __shfl_sync(0xffffffffu, v, 31);
+      run += __shfl_sync(kAll, v, 31);
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tm = S.tmem;
+  const uint32_t tm = __shfl_sync(kAll, S.tmem, 0);
   volatile int* const abort = &S.abort;
+  TreeCursor& cur = S.cur[warp];
+  TreeSeg& sg = S.seg[warp];
+  if (lane == 0) {
+    const unsigned U = (unsigned)pre[p.batch] * (unsigned)(L.H * p.chunks), W = (unsigned)tree_ctas(gridDim.x, U);
+    S.units = U;
+    S.ctas = W;
+    const unsigned c = blockIdx.x;
+    tree_cursor(p, pre, c < W ? tree_unit(U, W, c) : U, c < W ? tree_unit(U, W, c + 1) : U, cur);
+  }
+  __syncwarp();
 
-  const long long U = (long long)pre[p.batch] * L.H * p.chunks;
-  const long long W = tree_ctas(gridDim.x, U);
-  const long long cta = blockIdx.x;
-  const long long lo = cta < W ? U * cta / W : U, hi = cta < W ? U * (cta + 1) / W : U;
-  TreeCursor cur = tree_cursor(p, pre, lo, hi);
-  TreeSeg sg;
-
-  if (warp >= Sh::kDq + 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Sh::kRegIo));
-  else if (warp < Sh::kDq) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Sh::kRegDq));
-  else asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Sh::kRegSm));
-
-  if (warp == Sh::kDq + 9) {
-    // ======================= loader =======================
-    int slot = 0;
-    uint32_t ph = 1;  // the first pass over the slots finds them empty
-    int used = 0;
-    bool ok = true;
-    const __nv_bfloat16* sink[2] = {reinterpret_cast<const __nv_bfloat16*>(p.C.sink_k),
-                                    reinterpret_cast<const __nv_bfloat16*>(p.C.sink_v)};
-    const __nv_bfloat16* ring[2] = {reinterpret_cast<const __nv_bfloat16*>(p.C.resid_k),
-                                    reinterpret_cast<const __nv_bfloat16*>(p.C.resid_v)};
-    const __nv_bfloat16* draft[2] = {reinterpret_cast<const __nv_bfloat16*>(p.k_draft),
-                                     reinterpret_cast<const __nv_bfloat16*>(p.v_draft)};
-    while (ok && tree_next(p, pre, lens, cur, sg)) {
-      const long long pair = (long long)sg.b * L.H + sg.h;
-      for (int blk = sg.blk0; ok && blk < sg.blk1; ++blk) {
-        if (blk < sg.nq) {
-          const int ntile = (sg.ts.qn + 15) >> 4;
-          for (int half = 0; half < 2; ++half) {
-            if (!(ok = tree_wait(&S.slot_empty[slot], ph, abort, p.status))) break;
-            const int t0 = blk * 8 + half * 4;
-            // lane i < 4 owns tile t0 + i; a run of tiles of one record is one copy
-            const int t = t0 + lane;
-            uint32_t bytes = 0, hbytes = 0;
-            const uint8_t* rec = nullptr;
-            int run = 0, within = 0;
-            if (lane < 4 && t < ntile) {
-              const int r = t / L.tpg;
-              within = t - r * L.tpg;
-              if (lane == 0 || within == 0) {
-                rec = record_addr(L, p.C, sg.b, sg.h, r, p.status);
-                run = min(min(L.tpg - within, 4 - lane), ntile - t);
-                if (rec) {
-                  bytes = (uint32_t)(run * L.tile_bytes);
-                  hbytes = (uint32_t)L.hdr_bytes;
+  // (each role's branch begins with its register count, which the compiler then allocates by)
+  if (warp >= 16) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Sh::kRegIo));
+    if (warp == 16) {
+      // ======================= loader =======================
+      int slot = 0;
+      uint32_t ph = 1;  // the first pass over the slots finds them empty
+      int used = 0;
+      bool ok = true;
+      // half-warps copy the K and the V row of a bf16 token
+      const int kv = lane >> 4;
+      const __nv_bfloat16* const sink = reinterpret_cast<const __nv_bfloat16*>(kv ? p.C.sink_v : p.C.sink_k);
+      const __nv_bfloat16* const ring = reinterpret_cast<const __nv_bfloat16*>(kv ? p.C.resid_v : p.C.resid_k);
+      const __nv_bfloat16* const draft = reinterpret_cast<const __nv_bfloat16*>(kv ? p.v_draft : p.k_draft);
+      while (ok && tree_next(p, pre, lens, cur, sg)) {
+        const long long pair = (long long)sg.b * L.H + sg.h;
+        const int blk1 = sg.blk1, nq = sg.nq, qn = sg.qn;
+        for (int blk = sg.blk0; ok && blk < blk1; ++blk) {
+          if (blk < nq) {
+            const int ntile = (qn + 15) >> 4;
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {
+              if (!(ok = tree_wait(&S.slot_empty[slot], ph, abort, p.status))) break;
+              const int t0 = blk * 8 + half * 4;
+              // lane i < 4 owns tile t0 + i; a run of tiles of one record is one copy
+              const int t = t0 + lane;
+              uint32_t bytes = 0, hbytes = 0;
+              const uint8_t* rec = nullptr;
+              int run = 0, within = 0;
+              if (lane < 4 && t < ntile) {
+                const int r = t / L.tpg;
+                within = t - r * L.tpg;
+                if (lane == 0 || within == 0) {
+                  rec = record_addr(L, p.C, sg.b, sg.h, r, p.status);
+                  run = min(min(L.tpg - within, 4 - lane), ntile - t);
+                  if (rec) {
+                    bytes = (uint32_t)(run * L.tile_bytes);
+                    hbytes = (uint32_t)L.hdr_bytes;
+                  }
                 }
               }
+              uint32_t okmask = rec ? (((1u << run) - 1u) << lane) : 0u;
+              okmask = __reduce_or_sync(kAll, okmask);
+              const uint32_t total = __reduce_add_sync(kAll, bytes + hbytes);
+              const uint32_t bar = smem_addr(&S.slot_full[slot]);
+              uint8_t* const dst = slots + (size_t)slot * p.slot_bytes;
+              if (lane == 0) {
+                S.slot_ok[slot] = okmask;
+                mbar_arrive_expect_tx(bar, total);
+              }
+              __syncwarp();
+              if (rec) {
+                if (hbytes) bulk_copy_g2s(smem_addr(dst + (t / L.tpg - t0 / L.tpg) * 1024), rec, hbytes, bar);
+                bulk_copy_g2s(smem_addr(dst + p.slot_hdr + lane * L.tile_bytes),
+                              rec + L.hdr_bytes + (long long)within * L.tile_bytes, bytes, bar);
+              }
+              if (lane != 0) mbar_arrive(bar);
+              if (++slot == p.nslots) { slot = 0; ph ^= 1; }
+              ++used;
             }
-            uint32_t okmask = rec ? (((1u << run) - 1u) << lane) : 0u;
-            okmask = __reduce_or_sync(0xffffffffu, okmask);
-            const uint32_t total = __reduce_add_sync(0xffffffffu, bytes + hbytes);
-            const uint32_t bar = smem_addr(&S.slot_full[slot]);
-            uint8_t* const dst = slots + (size_t)slot * p.slot_bytes;
-            if (lane == 0) {
-              S.slot_ok[slot] = okmask;
-              mbar_arrive_expect_tx(bar, total);
-            }
-            __syncwarp();
-            if (rec) {
-              if (hbytes) bulk_copy_g2s(smem_addr(dst + (t / L.tpg - t0 / L.tpg) * 1024), rec, hbytes, bar);
-              bulk_copy_g2s(smem_addr(dst + p.slot_hdr + lane * L.tile_bytes),
-                            rec + L.hdr_bytes + (long long)within * L.tile_bytes, bytes, bar);
-            }
-            if (lane != 0) mbar_arrive(bar);
-            if (++slot == p.nslots) { slot = 0; ph ^= 1; }
-            ++used;
-          }
-        } else {
-          const int x0 = (blk - sg.nq) * kBlk;
-          const int nsr = sg.ts.n_sink + sg.ts.r, nrow = nsr + p.N;
-          for (int part = 0; part < kBlk; part += p.bf_tokens) {
-            if (!(ok = tree_wait(&S.slot_empty[slot], ph, abort, p.status))) break;
-            uint8_t* const dst = slots + (size_t)slot * p.slot_bytes;
-            const int c = lane & 15;
+          } else {
+            const int x0 = (blk - nq) * kBlk, n_sink = sg.n_sink;
+            const int nsr = n_sink + sg.r, nrow = nsr + p.N;
+            for (int part = 0; part < kBlk; part += p.bf_tokens) {
+              if (!(ok = tree_wait(&S.slot_empty[slot], ph, abort, p.status))) break;
+              uint8_t* const dst = slots + (size_t)slot * p.slot_bytes;
+              const int c = lane & 15;
+              int at = x0 + part - n_sink;  // ring slot of the first row (rows before it do not use it)
+              at = (int)(((long long)qn + (at < 0 ? 0 : at)) % (L.W > 0 ? L.W : 1));
 #pragma unroll 4
-            for (int i = 0; i < p.bf_tokens; ++i) {  // half-warps copy the K and the V row of a token
-              const int kv = lane >> 4;
-              const int x = x0 + part + i;
-              const __nv_bfloat16* src = draft[kv];
-              uint32_t n = 16;
-              if (x < sg.ts.n_sink) src = sink[kv] + (pair * L.S + x) * L.d;
-              else if (x < nsr) src = ring[kv] + (pair * L.W + (sg.ts.qn + (x - sg.ts.n_sink)) % L.W) * L.d;
-              else if (x < nrow) src = draft[kv] + (pair * p.N + (x - nsr)) * L.d;
-              else n = 0;  // rows behind the list: zeros
-              const uint32_t to = smem_addr(dst) + (kv ? p.bf_tokens * 256 + vrow_chunk(i, c) : krow_chunk(i, c));
-              asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(src + c * 8), "r"(n)
+              for (int i = 0; i < p.bf_tokens; ++i) {
+                const int x = x0 + part + i;
+                const __nv_bfloat16* src = draft;
+                uint32_t n = 16;
+                if (x < n_sink) src = sink + (pair * L.S + x) * L.d;
+                else if (x < nsr) {
+                  src = ring + (pair * L.W + at) * L.d;
+                  if (++at == L.W) at = 0;
+                } else if (x < nrow) src = draft + (pair * p.N + (x - nsr)) * L.d;
+                else n = 0;  // rows behind the list: zeros
+                const uint32_t to = smem_addr(dst) + (kv ? p.bf_tokens * 256 + vrow_chunk(i, c) : krow_chunk(i, c));
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(src + c * 8), "r"(n)
+                             : "memory");
+              }
+              asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
+                               smem_addr(&S.slot_full[slot]))
                            : "memory");
+              if (++slot == p.nslots) { slot = 0; ph ^= 1; }
+              ++used;
             }
-            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
-                             smem_addr(&S.slot_full[slot]))
-                         : "memory");
-            if (++slot == p.nslots) { slot = 0; ph ^= 1; }
-            ++used;
           }
         }
       }
-    }
-    // every copy must have landed before the CTA ends (bounded; the consumers waited for all of
-    // them unless the launch was given up)
-    asm volatile("cp.async.wait_all;" ::: "memory");
-    if (*abort) {
-      for (int i = 0; i < p.nslots && i < used; ++i) {
-        const int n = used - 1 - i;  // the slot's last use
-        mbar_wait_bounded(smem_addr(&S.slot_full[n % p.nslots]), (n / p.nslots) & 1, kTreeWait);
+      // every copy must have landed before the CTA ends (bounded; the consumers waited for all of
+      // them unless the launch was given up)
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      if (*abort) {
+        for (int i = 0; i < p.nslots && i < used; ++i) {
+          const int n = used - 1 - i;  // the slot's last use
+          mbar_wait_bounded(smem_addr(&S.slot_full[n % p.nslots]), (n / p.nslots) & 1, kTreeWait);
+        }
       }
-    }
-  } else if (warp == Sh::kDq + 8) {
-    // ======================= MMA issue (one thread) =======================
-    if (lane == 0) {
-      constexpr uint32_t kIdQk = mma_idesc(SUB, 0), kIdPv = mma_idesc(SUB, 1);
-      constexpr uint32_t kSwP = SUB == 64 ? 2 : (SUB == 32 ? 4 : 6);
-      constexpr uint32_t kPRow = SUB * 2;
-      uint64_t dq[2], dp[2];
-      for (int h = 0; h < 2; ++h) {
-        dq[h] = smem_desc(smem_addr(Qs + h * Sh::kQBytes), 16, 1024, 2);
-        dp[h] = smem_desc(smem_addr(Ps + h * Sh::kPBytes), 8 * kPRow, 8 * kPRow, kSwP);
-      }
-      long long g = 0;  // blocks so far
-      uint32_t nseg = 0;
+    } else if (warp == 17) {
+      // ======================= MMA =======================
+      // (the whole warp walks, so that the operands of the one-thread instructions stay uniform)
+      constexpr uint32_t kIdQk = mma_idesc(NT, 0), kIdPv = mma_idesc(NT, 1);
+      const uint64_t dq = smem_desc(smem_addr(Qs), 16, 1024, 2);
+      const uint64_t dp = smem_desc(smem_addr(Ps), kBlk * 128, 8 * Sh::kPRow, Sh::kPSwizzle);
+      uint32_t g = 0, nseg = 0;  // blocks and cuts so far
       bool ok = true;
       while (ok && tree_next(p, pre, lens, cur, sg)) {
-        const int nb = sg.blk1 - sg.blk0;
-        for (int h = 0; h < 2 && ok; ++h) ok = tree_wait(&S.q_full[h], nseg & 1, abort, p.status);
+        const int nb = __shfl_sync(kAll, sg.blk1 - sg.blk0, 0);
+        ok = __all_sync(kAll, tree_wait(&S.q_full, nseg & 1, abort, p.status));
         ++nseg;
+#pragma unroll 1
         for (int i = 0; ok && i <= nb; ++i) {
           if (i < nb) {
-            const int kb = (int)(g & 1);
-            if (!(ok = tree_wait(&S.k_full[kb], (uint32_t)(g >> 1) & 1, abort, p.status))) break;
-            for (int h = 0; h < 2; ++h) {
-              if (g > 0 && !(ok = tree_wait(&S.s_free[h], (uint32_t)(g - 1) & 1, abort, p.status))) break;
-              tc_fence_after();
+            const uint32_t kb = Sh::kKv == 2 ? g & 1 : 0, kph = Sh::kKv == 2 ? (g >> 1) & 1 : g & 1, sb = g & 1;
+            ok = tree_wait(&S.k_full[kb], kph, abort, p.status);
+            if (ok && g > 1) ok = tree_wait(&S.s_free[sb], ((g >> 1) - 1) & 1, abort, p.status);
+            if (!__all_sync(kAll, ok)) { ok = false; break; }
+            tc_fence_after();
+            if (elect_one()) {
 #pragma unroll
               for (int s = 0; s < 8; ++s)
-                tc_mma_ts(tm + kTmS + h * 64, tm + kTmK + kb * 64 + 8 * s,
-                          dq[h] + (uint64_t)(((s >> 2) * SUB * 128 + (s & 3) * 32) >> 4), kIdQk, s > 0);
-              tc_commit(smem_addr(&S.s_full[h]));
+                tc_mma_ts(tm + Sh::kTmS + sb * NT, tm + Sh::kTmK + kb * 64 + 8 * s,
+                          dq + (uint32_t)(((s >> 2) * NT * 128 + (s & 3) * 32) >> 4), kIdQk, s > 0);
+              tc_commit(smem_addr(&S.s_full[sb]));
+              tc_commit(smem_addr(&S.k_empty[kb]));
             }
-            if (!ok) break;
-            tc_commit(smem_addr(&S.k_empty[kb]));
+            __syncwarp();
           }
           if (i > 0) {
-            const long long pg = g - 1;
-            const int vb = (int)(pg & 1);
-            if (!(ok = tree_wait(&S.v_full[vb], (uint32_t)(pg >> 1) & 1, abort, p.status))) break;
-            for (int h = 0; h < 2; ++h) {
-              if (!(ok = tree_wait(&S.p_full[h], (uint32_t)pg & 1, abort, p.status))) break;
-              tc_fence_after();
+            const uint32_t pg = g - 1, vb = Sh::kKv == 2 ? pg & 1 : 0, vph = Sh::kKv == 2 ? (pg >> 1) & 1 : pg & 1,
+                           pb = pg & 1;
+            ok = tree_wait(&S.v_full[vb], vph, abort, p.status);
+            if (ok) ok = tree_wait(&S.p_full[pb], (pg >> 1) & 1, abort, p.status);
+            if (!__all_sync(kAll, ok)) { ok = false; break; }
+            tc_fence_after();
+            if (elect_one()) {
 #pragma unroll
               for (int j = 0; j < 8; ++j)
-                tc_mma_ts(tm + kTmO + h * 64, tm + kTmV + vb * 64 + 8 * j,
-                          dp[h] + (uint64_t)((j * 16 * kPRow) >> 4), kIdPv, (i > 1 || j > 0) ? 1u : 0u);
-              tc_commit(smem_addr(&S.p_free[h]));
+                tc_mma_ts(tm + Sh::kTmO, tm + Sh::kTmV + vb * 64 + 8 * j,
+                          dp + (uint32_t)((pb * Sh::kPBytes + j * 16 * Sh::kPRow) >> 4), kIdPv,
+                          (i > 1 || j > 0) ? 1u : 0u);
+              tc_commit(smem_addr(&S.p_free[pb]));
+              tc_commit(smem_addr(&S.v_empty[vb]));
             }
-            if (!ok) break;
-            tc_commit(smem_addr(&S.v_empty[vb]));
+            __syncwarp();
           }
           if (i < nb) ++g;
         }
       }
-      if (!ok) {  // given up: let the products in flight end before the tensor memory is freed
+      if (!ok && elect_one()) {  // given up: let the products in flight end before the tensor memory is freed
         tc_commit(smem_addr(&S.drain));
         mbar_wait_bounded(smem_addr(&S.drain), 0, kTreeWait);
       }
+      __syncwarp();
+    } else if (!F::kFp8 && warp == 18) {
+      // ======================= check: scales that leave f16 =======================
+      // a group's values are s (n - z) with n in [0, L]
+      constexpr float kL = (float)((1 << F::kBits) - 1);
+      int slot = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      float worst = 0.f;
+      while (ok && tree_next(p, pre, lens, cur, sg)) {
+        const int blk1 = sg.blk1, nq = sg.nq;
+        for (int blk = sg.blk0; ok && blk < blk1; ++blk) {
+          const bool quant = blk < nq;
+          const int n = quant ? 2 : kBlk / p.bf_tokens;
+          for (int i = 0; i < n; ++i) {
+            if (!(ok = tree_wait(&S.slot_full[slot], ph, abort, p.status))) break;
+            const uint32_t okmask = S.slot_ok[slot];
+            if (quant) {
+              const uint8_t* const src = slots + (size_t)slot * p.slot_bytes;
+              const int t0 = blk * 8 + i * 4;
+              for (int ti = 0; ti < 4; ++ti) {
+                if (!((okmask >> ti) & 1u)) continue;
+                if (ti == 0 || (t0 + ti) % L.tpg == 0) {
+                  const float* hdr = reinterpret_cast<const float*>(src + ((t0 + ti) / L.tpg - t0 / L.tpg) * 1024);
+#pragma unroll
+                  for (int c = 0; c < 128; c += 32) worst = fmaxf(worst, group_reach(hdr[c + lane], hdr[128 + c + lane], kL));
+                }
+                const float* vs =
+                    reinterpret_cast<const float*>(src + p.slot_hdr + ti * L.tile_bytes + 32 * F::kRb);
+                for (int c = lane; c < 16 * L.ngv; c += 32) worst = fmaxf(worst, group_reach(vs[c], vs[16 * L.ngv + c], kL));
+              }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&S.slot_empty[slot]));
+            if (++slot == p.nslots) { slot = 0; ph ^= 1; }
+          }
+        }
+      }
+      if (__any_sync(kAll, worst >= 65520.f) && lane == 0) report(p.status, KVQ_DEV_RANGE);
     }
-    __syncwarp();
-  } else if (warp < Sh::kDq) {
+  } else if (warp < 8) {
     // ======================= dequantization =======================
-    const int wq = warp & 3;                       // tensor-memory lanes 32 wq ..
-    const bool doK = warp < 4, doV = Sh::kDq == 4 || warp >= 4;
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Sh::kRegDq));
+    const int wq = warp & 3;  // tensor-memory lanes 32 wq ..
+    const bool isV = warp >= 4;
     const int r = lane >> 2, q = lane & 3;
-    const uint32_t tlane = tm + ((uint32_t)(32 * wq) << 16);
+    const uint32_t tlane = tm + ((uint32_t)(32 * wq) << 16) + (isV ? Sh::kTmV : Sh::kTmK);
+    unsigned long long* const full = isV ? S.v_full : S.k_full;
+    unsigned long long* const empty = isV ? S.v_empty : S.k_empty;
     int slot = 0;
-    uint32_t ph = 0;
-    long long g = 0;
-    bool ok = true;
-    uint32_t bad = 0;
-    float vinv = 1.f;
-    if constexpr (F::kFp8) vinv = 1.f / (*p.C.v_tscale * (FMT == KVQ_FMT_FP8_E5M2 ? 256.f : 1.f));
+    uint32_t ph = 0, g = 0;
+    bool ok = true, bad = false;
     while (ok && tree_next(p, pre, lens, cur, sg)) {
-      for (int blk = sg.blk0; ok && blk < sg.blk1; ++blk, ++g) {
-        const int buf = (int)(g & 1);
-        const uint32_t eph = ((uint32_t)(g >> 1) & 1) ^ 1;  // the buffer's previous use has been read
-        if (doK) ok = tree_wait(&S.k_empty[buf], eph, abort, p.status);
-        if (ok && doV) ok = tree_wait(&S.v_empty[buf], eph, abort, p.status);
-        if (!ok) break;
+      const int blk1 = sg.blk1, nq = sg.nq;
+#pragma unroll 1
+      for (int blk = sg.blk0; ok && blk < blk1; ++blk, ++g) {
+        const int buf = Sh::kKv == 2 ? (int)(g & 1) : 0;
+        // the buffer's previous use has been read
+        if (!(ok = tree_wait(&empty[buf], (Sh::kKv == 2 ? (g >> 1) & 1 : g & 1) ^ 1, abort, p.status))) break;
         tc_fence_after();
-        const uint32_t tk = tlane + kTmK + buf * 64, tv = tlane + kTmV + buf * 64;
-        if (blk < sg.nq) {
+        const uint32_t tt = tlane + buf * 64;
+        if (blk < nq) {
+#pragma unroll 1
           for (int half = 0; half < 2; ++half) {
             if (!(ok = tree_wait(&S.slot_full[slot], ph, abort, p.status))) break;
             const uint8_t* const src = slots + (size_t)slot * p.slot_bytes;
             const uint32_t okmask = S.slot_ok[slot];
             const int t0 = blk * 8 + half * 4;
-            if (doK && (wq >> 1) == half) {
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const int ti = 2 * (wq & 1) + e;  // tile of the slot
-                if ((okmask >> ti) & 1u) {
+            if (!isV) {
+              if ((wq >> 1) == half) {
+#pragma unroll 1
+                for (int e = 0; e < 2; ++e) {
+                  const int ti = 2 * (wq & 1) + e;  // tile of the slot
+                  if (!((okmask >> ti) & 1u)) continue;
                   const float* hdr = nullptr;
-                  if constexpr (!F::kFp8) {
+                  if constexpr (!F::kFp8)
                     hdr = reinterpret_cast<const float*>(src + ((t0 + ti) / L.tpg - t0 / L.tpg) * 1024);
-                    // a Key beyond f16: its scale group says so
-                    const float4 sc = *reinterpret_cast<const float4*>(hdr + 4 * lane);
-                    const float4 z = *reinterpret_cast<const float4*>(hdr + 128 + 4 * lane);
-                    constexpr float kL = (float)((1 << F::kBits) - 1);
-                    const float m = fmaxf(fmaxf(fabsf(sc.x) * fmaxf(fabsf(z.x), fabsf(kL - z.x)),
-                                                fabsf(sc.y) * fmaxf(fabsf(z.y), fabsf(kL - z.y))),
-                                          fmaxf(fabsf(sc.z) * fmaxf(fabsf(z.z), fabsf(kL - z.z)),
-                                                fabsf(sc.w) * fmaxf(fabsf(z.w), fabsf(kL - z.w))));
-                    if (m >= 65520.f) bad = 1;
-                  }
                   uint32_t w[F::kWords];
                   load_words<FMT>(src + p.slot_hdr + ti * L.tile_bytes, lane, w);
 #pragma unroll
                   for (int i = 0; i < 2; ++i) {
                     uint32_t f[16];
                     k_frags<FMT>(w, hdr, i, q, f);
-                    tc_st_frag4(tk + ((uint32_t)(16 * e) << 16) + 32 * i, f);
+                    tc_st_frag4(tt + ((uint32_t)(16 * e) << 16) + 32 * i, f);
                   }
                 }
               }
-            }
-            if (doV) {
+            } else {
               const int ngv = F::kFp8 ? 1 : L.ngv;
+#pragma unroll 1
+              for (int tp = 0; tp < 4; tp += 2) {  // two tiles, channels 32 wq .. and 32 wq + 16 ..
+                uint32_t f[2][8];
 #pragma unroll
-              for (int e = 0; e < 2; ++e) {  // channels 32 wq + 16 e ..
-                const int s = 2 * wq + e;
-                uint32_t f[16];
+                for (int u = 0; u < 2; ++u) {
+                  const int ti = tp + u;
+                  // not in the store (behind the last tile, or a bad block): P is 0 there, so V must be finite
 #pragma unroll
-                for (int ti = 0; ti < 4; ++ti) {
+                  for (int e = 0; e < 2; ++e) f[e][4 * u] = f[e][4 * u + 1] = f[e][4 * u + 2] = f[e][4 * u + 3] = 0u;
                   if ((okmask >> ti) & 1u) {
-                    const uint8_t* tile = src + p.slot_hdr + ti * L.tile_bytes;
-                    const uint8_t* codes = tile + 16 * F::kRb;
-                    // the words of step s only
-                    uint32_t w2[2];
+                    const uint8_t* const tile = src + p.slot_hdr + ti * L.tile_bytes;
+                    const uint8_t* const codes = tile + 16 * F::kRb;
+                    uint32_t w[4];  // the words of steps 2 wq and 2 wq + 1
                     if constexpr (F::kBits == 8) {
-                      const uint2 v = *reinterpret_cast<const uint2*>(codes + ((s >> 1) * 32 + lane) * 16 + (s & 1) * 8);
-                      w2[0] = v.x;
-                      w2[1] = v.y;
+                      const uint4 v = *reinterpret_cast<const uint4*>(codes + (wq * 32 + lane) * 16);
+                      w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
                     } else if constexpr (F::kBits == 4) {
-                      w2[0] = *reinterpret_cast<const uint32_t*>(codes + ((s >> 2) * 32 + lane) * 16 + (s & 3) * 4);
+                      const uint2 v =
+                          *reinterpret_cast<const uint2*>(codes + ((wq >> 1) * 32 + lane) * 16 + (wq & 1) * 8);
+                      w[0] = v.x, w[1] = v.y;
                     } else {
-                      w2[0] = *reinterpret_cast<const uint32_t*>(codes + lane * 16 + (s >> 1) * 4) >> (8 * (s & 1));
+                      w[0] = *reinterpret_cast<const uint32_t*>(codes + lane * 16 + wq * 4);
+                      w[1] = w[0] >> 8;
                     }
                     float4 sc = make_float4(1.f, 1.f, 1.f, 1.f), nz = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if constexpr (!F::kFp8) {
-                      const float* vs = reinterpret_cast<const float*>(tile + 32 * F::kRb) + (16 * s) / L.Gv;
-                      const float* vz = vs + 16 * ngv;
-                      sc = make_float4(vs[(2 * q) * ngv], vs[(2 * q + 1) * ngv], vs[(2 * q + 8) * ngv],
-                                       vs[(2 * q + 9) * ngv]);
-                      const float4 z = make_float4(vz[(2 * q) * ngv], vz[(2 * q + 1) * ngv], vz[(2 * q + 8) * ngv],
-                                                   vz[(2 * q + 9) * ngv]);
-                      nz = make_float4(-sc.x * z.x, -sc.y * z.y, -sc.z * z.z, -sc.w * z.w);
-                      constexpr float kL = (float)((1 << F::kBits) - 1);
-                      const float m = fmaxf(fmaxf(fmaxf(fabsf(nz.x), fabsf(fmaf(kL, sc.x, nz.x))),
-                                                  fmaxf(fabsf(nz.y), fabsf(fmaf(kL, sc.y, nz.y)))),
-                                            fmaxf(fmaxf(fabsf(nz.z), fabsf(fmaf(kL, sc.z, nz.z))),
-                                                  fmaxf(fabsf(nz.w), fabsf(fmaf(kL, sc.w, nz.w)))));
-                      if (m >= 65520.f) bad = 1;
-                    }
-                    v_frag<FMT>(w2, 0, sc, nz, f + 4 * ti);
+                    const float* const vs = reinterpret_cast<const float*>(tile + 32 * F::kRb);
+                    if constexpr (!F::kFp8) value_scales(vs, ngv, (32 * wq) / L.Gv, q, sc, nz);
+                    v_frag<FMT>(w, 0, sc, nz, f[0] + 4 * u);
+                    if constexpr (!F::kFp8)
+                      if (L.Gv == 16) value_scales(vs, ngv, 2 * wq + 1, q, sc, nz);
+                    v_frag<FMT>(w + (F::kBits == 8 ? 2 : 1), 0, sc, nz, f[1] + 4 * u);
                     if constexpr (F::kFp8) {
                       // tokens behind the last one of a partly filled tile: zeros whatever the store holds
-                      const int nv = sg.ts.qn - 16 * (t0 + ti);
+                      const int nv = sg.qn - 16 * (t0 + ti);
                       if (nv < 16) {
-                        if (2 * q >= nv) f[4 * ti] = f[4 * ti + 1] = 0u;
-                        else if (2 * q + 1 >= nv) { f[4 * ti] &= 0xFFFFu; f[4 * ti + 1] &= 0xFFFFu; }
-                        if (2 * q + 8 >= nv) f[4 * ti + 2] = f[4 * ti + 3] = 0u;
-                        else if (2 * q + 9 >= nv) { f[4 * ti + 2] &= 0xFFFFu; f[4 * ti + 3] &= 0xFFFFu; }
+                        const uint32_t m0 = pair_mask(2 * q, nv), m1 = pair_mask(2 * q + 8, nv);
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                          f[e][4 * u] &= m0, f[e][4 * u + 1] &= m0;
+                          f[e][4 * u + 2] &= m1, f[e][4 * u + 3] &= m1;
+                        }
                       }
                     }
-                  } else {  // not in the store (behind the last tile, or a bad block): P is 0 there, so V must be finite
-                    f[4 * ti] = f[4 * ti + 1] = f[4 * ti + 2] = f[4 * ti + 3] = 0u;
                   }
                 }
-                tc_st_frag4(tv + ((uint32_t)(16 * e) << 16) + 32 * half, f);
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                  tc_st_frag2(tt + ((uint32_t)(16 * e) << 16) + 32 * half + 8 * tp, f[e]);
               }
             }
             __syncwarp();
@@ -724,36 +824,38 @@ __global__ void __launch_bounds__(TreeShape<SUB>::kThreads, 1) tree_kernel(const
             if (++slot == p.nslots) { slot = 0; ph ^= 1; }
           }
         } else {
-          uint32_t km = 0, vm = 0;
-          const bool drafts = (blk - sg.nq) * kBlk + kBlk > sg.ts.n_sink + sg.ts.r;
+          uint32_t top = 0;
+          const bool drafts = (blk - nq) * kBlk + kBlk > sg.n_sink + sg.r;
+          const float vinv = F::kFp8 && isV ? 1.f / (*p.C.v_tscale * (FMT == KVQ_FMT_FP8_E5M2 ? 256.f : 1.f)) : 1.f;
+#pragma unroll 1
           for (int part = 0; part < kBlk; part += p.bf_tokens) {
             if (!(ok = tree_wait(&S.slot_full[slot], ph, abort, p.status))) break;
             const uint8_t* const src = slots + (size_t)slot * p.slot_bytes;
-            if (doK && 32 * wq >= part && 32 * wq < part + p.bf_tokens) {
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const int row = 32 * wq - part + 16 * e + r;
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
+            if (!isV) {
+              if (32 * wq >= part && 32 * wq < part + p.bf_tokens) {
+#pragma unroll 1
+                for (int ei = 0; ei < 4; ++ei) {  // 16 rows, four steps
+                  const int e = ei >> 1, i = ei & 1;
+                  const int row = 32 * wq - part + 16 * e + r;
                   uint32_t f[16];
 #pragma unroll
                   for (int j = 0; j < 4; ++j) {
                     const int c = 2 * (4 * i + j) + (q >> 1);
                     const uint2 a = *reinterpret_cast<const uint2*>(src + krow_chunk(row, c) + (q & 1) * 8);
                     const uint2 b = *reinterpret_cast<const uint2*>(src + krow_chunk(row + 8, c) + (q & 1) * 8);
-                    km = abs_max2(abs_max2(abs_max2(abs_max2(km, a.x), a.y), b.x), b.y);
+                    top = abs_max2(abs_max2(abs_max2(abs_max2(top, a.x), a.y), b.x), b.y);
                     f[4 * j] = bf16x2_to_f16x2(a.x);
                     f[4 * j + 1] = bf16x2_to_f16x2(b.x);
                     f[4 * j + 2] = bf16x2_to_f16x2(a.y);
                     f[4 * j + 3] = bf16x2_to_f16x2(b.y);
                   }
-                  tc_st_frag4(tk + ((uint32_t)(16 * e) << 16) + 32 * i, f);
+                  tc_st_frag4(tt + ((uint32_t)(16 * e) << 16) + 32 * i, f);
                 }
               }
-            }
-            if (doV) {
+            } else {
               const uint32_t vbase = smem_addr(src) + p.bf_tokens * 256;
               const int row0 = (lane & 7) + ((lane >> 4) << 3), cc = (lane >> 3) & 1;
+#pragma unroll 1
               for (int t4 = 0; t4 < p.bf_tokens; t4 += 32) {  // two fragments of 16 tokens at a time
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
@@ -765,20 +867,20 @@ __global__ void __launch_bounds__(TreeShape<SUB>::kThreads, 1) tree_kernel(const
                     ldmatrix_x4_trans(vbase + vrow_chunk(t4 + 16 * u + row0, c), a[0], a[1], a[2], a[3]);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                      vm = abs_max2(vm, a[i]);
-                      uint32_t v = F::kFp8 ? bf16x2_to_f16x2(a[i], vinv) : bf16x2_to_f16x2(a[i]);
-                      if (drafts) {
-                        if ((v & 0x7C00u) == 0x7C00u) v &= 0xFFFF0000u;
-                        if ((v & 0x7C000000u) == 0x7C000000u) v &= 0xFFFFu;
-                      }
-                      f[4 * u + i] = v;
+                      top = abs_max2(top, a[i]);
+                      f[4 * u + i] = F::kFp8 ? bf16x2_to_f16x2(a[i], vinv) : bf16x2_to_f16x2(a[i]);
                     }
                   }
-                  asm volatile(
-                      "tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(
-                          tv + ((uint32_t)(16 * e) << 16) + ((part + t4) >> 1)),
-                      "r"(f[0]), "r"(f[1]), "r"(f[2]), "r"(f[3]), "r"(f[4]), "r"(f[5]), "r"(f[6]), "r"(f[7])
-                      : "memory");
+                  if (drafts) {
+                    // a drafted Value that f16 does not hold: zero, so that the nodes that do not see
+                    // its token do not get 0 * NaN (those that do get NaN through P)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                      if ((f[i] & 0x7C00u) == 0x7C00u) f[i] &= 0xFFFF0000u;
+                      if ((f[i] & 0x7C000000u) == 0x7C000000u) f[i] &= 0xFFFFu;
+                    }
+                  }
+                  tc_st_frag2(tt + ((uint32_t)(16 * e) << 16) + ((part + t4) >> 1), f);
                 }
               }
             }
@@ -787,248 +889,245 @@ __global__ void __launch_bounds__(TreeShape<SUB>::kThreads, 1) tree_kernel(const
             if (++slot == p.nslots) { slot = 0; ph ^= 1; }
           }
           // a bf16 value that f16 does not hold (65504 is the last one)
-          const float kx = __uint_as_float(max(km & 0xFFFFu, km >> 16) << 16);
-          const float vx = __uint_as_float(max(vm & 0xFFFFu, vm >> 16) << 16) * fabsf(vinv);
-          if (!(kx < 65520.f) || !(vx < 65520.f)) bad = 1;
+          if (!(__uint_as_float(max(top & 0xFFFFu, top >> 16) << 16) * fabsf(vinv) < 65520.f)) bad = true;
         }
         if (!ok) break;
         tc_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          if (doK) mbar_arrive(smem_addr(&S.k_full[buf]));
-          if (doV) mbar_arrive(smem_addr(&S.v_full[buf]));
-        }
+        if (lane == 0) mbar_arrive(smem_addr(&full[buf]));
       }
     }
-    if (__any_sync(0xffffffffu, bad) && lane == 0) report(p.status, KVQ_DEV_RANGE);
-  } else if (warp < Sh::kDq + 8) {
+    if (__any_sync(kAll, bad) && lane == 0) report(p.status, KVQ_DEV_RANGE);
+  } else {
     // ======================= softmax, epilogue =======================
-    const int h = (warp - Sh::kDq) >> 2;    // column half
-    const int tok = tid - 32 * Sh::kDq - 128 * h;  // 0 .. 127: the thread's tensor-memory lane
-    const int wq = tok >> 5;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Sh::kRegSm));
+    const int h = (warp - 8) >> 2;        // column half
+    const int wq = warp & 3;
+    const int tok = 32 * wq + lane;       // the thread's tensor-memory lane: token of the scores, channel of the outputs
+    const int th = tid - 256;             // 0 .. 255 over both halves
     const uint32_t tlane = tm + ((uint32_t)(32 * wq) << 16);
-    const uint32_t ts_ = tlane + kTmS + h * 64, to_ = tlane + kTmO + h * 64;
-    uint8_t* const Q = Qs + h * Sh::kQBytes;
-    uint8_t* const P = Ps + h * Sh::kPBytes;
-    float* const ms = S.m[h];
+    float* const ms = S.m + h * SUB;
     const int barid = 1 + h;
-    const float vunit = F::kFp8 ? *p.C.v_tscale * (FMT == KVQ_FMT_FP8_E5M2 ? 256.f : 1.f) : 1.f;
-    const float cq = F::kFp8 ? p.scale_log2 * *p.C.k_tscale : p.scale_log2;
-    long long g = 0;
-    uint32_t bad = 0;
+    uint32_t g = 0;
     while (tree_next(p, pre, lens, cur, sg)) {
-      const int col0 = (sg.ch * 2 + h) * SUB;  // first column of this half
-      const int C = p.gh * p.N;
-      // ---- the drafted tokens, where this segment reaches a block of theirs ----
-      const bool has_tree = sg.blk1 > sg.nq + (sg.ts.n_sink + sg.ts.r) / kBlk;
-      bool wild = false;
-      if (has_tree && tok < p.N) {
-        int up = p.parents[(long long)sg.b * p.N + tok];
-        if (up < -1 || up >= tok) {
-          report(p.status, KVQ_DEV_BAD_TREE);
-          up = -1;
+      // ---- the drafted tokens, where this cut reaches a block of theirs ----
+      named_sync(3, 256);  // (the previous cut's epilogue has read S.m)
+      if (th < NT) S.m[th] = 0.f;
+      if (th < 64 && sg.blk1 > sg.nq + (sg.n_sink + sg.r) / kBlk) {
+        bool wild = false;
+        if (th < p.N) {
+          int up = p.parents[(long long)sg.b * p.N + th];
+          if (up < -1 || up >= th) {
+            report(p.status, KVQ_DEV_BAD_TREE);
+            up = -1;
+          }
+          S.par[th] = up;
+          const float vinv = F::kFp8 ? 1.f / (*p.C.v_tscale * (FMT == KVQ_FMT_FP8_E5M2 ? 256.f : 1.f)) : 1.f;
+          const uint4* v = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.v_draft) +
+                                                          (((long long)sg.b * L.H + sg.h) * p.N + th) * L.d);
+          uint32_t m = 0;
+#pragma unroll 8
+          for (int i = 0; i < 16; ++i) {
+            const uint4 a = v[i];
+            m = abs_max2(abs_max2(abs_max2(abs_max2(m, a.x), a.y), a.z), a.w);
+          }
+          wild = !(__uint_as_float(max(m & 0xFFFFu, m >> 16) << 16) * fabsf(vinv) < 65520.f);
         }
-        S.par[h][tok] = up;
-        // (its Values are replaced by zeros, see the dequantization: the nodes that do not see them
-        // must not get 0 * NaN; the ones that do get NaN through P)
-        const uint4* v = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.v_draft) +
-                                                        (((long long)sg.b * L.H + sg.h) * p.N + tok) * L.d);
-        uint32_t m = 0;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const uint4 a = v[i];
-          m = abs_max2(abs_max2(abs_max2(abs_max2(m, a.x), a.y), a.z), a.w);
-        }
-        wild = !(__uint_as_float(max(m & 0xFFFFu, m >> 16) << 16) * fabsf(1.f / vunit) < 65520.f);
+        const uint32_t w = __ballot_sync(kAll, wild);
+        if (lane == 0) reinterpret_cast<uint32_t*>(&S.wild)[wq] = w;
       }
-      // ---- the half's queries, f16, channels in the Key fragments' order within every 16 ----
-      for (int i = tok; i < SUB * 8; i += 128) {
-        const int row = i >> 3, g16 = i & 7;
-        const int col = col0 + row;
-        uint4 a = make_uint4(0, 0, 0, 0), b = a;
-        if (col < C) {
-          const int n = col / p.gh, hh = col - n * p.gh;
-          const uint4* src = reinterpret_cast<const uint4*>(
-              reinterpret_cast<const __nv_bfloat16*>(p.q) +
-              (((long long)sg.b * p.N + n) * p.Hq + (long long)sg.h * p.gh + hh) * L.d + 16 * g16);
-          a = src[0];
-          b = src[1];
+      // ---- the queries, f16, channels in the Key fragments' order within every 16 ----
+      {
+        uint32_t m = 0;
+        const int g16 = th & 7;
+#pragma unroll 1
+        for (int row = th >> 3; row < NT; row += 32) {
+          const int col = sg.ch * NT + row;
+          uint4 a = make_uint4(0, 0, 0, 0), b = a;
+          if (col < p.gh * p.N) {
+            const int n = col / p.gh, hh = col - n * p.gh;
+            const uint4* src = reinterpret_cast<const uint4*>(
+                reinterpret_cast<const __nv_bfloat16*>(p.q) +
+                (((long long)sg.b * p.N + n) * p.Hq + (long long)sg.h * p.gh + hh) * L.d + 16 * g16);
+            a = src[0];
+            b = src[1];
+          }
+          m = abs_max2(abs_max2(abs_max2(abs_max2(m, a.x), a.y), a.z), a.w);
+          m = abs_max2(abs_max2(abs_max2(abs_max2(m, b.x), b.y), b.z), b.w);
+          uint8_t* const dst = Qs + (g16 >> 2) * (NT * 128) + row * 128;
+          const int c = 2 * (g16 & 3);
+          *reinterpret_cast<uint4*>(dst + ((c ^ (row & 7)) << 4)) = make_uint4(
+              bf16x2_to_f16x2(a.x), bf16x2_to_f16x2(a.z), bf16x2_to_f16x2(b.x), bf16x2_to_f16x2(b.z));
+          *reinterpret_cast<uint4*>(dst + (((c + 1) ^ (row & 7)) << 4)) = make_uint4(
+              bf16x2_to_f16x2(a.y), bf16x2_to_f16x2(a.w), bf16x2_to_f16x2(b.y), bf16x2_to_f16x2(b.w));
         }
-        uint32_t m = abs_max2(abs_max2(abs_max2(abs_max2(0u, a.x), a.y), a.z), a.w);
-        m = abs_max2(abs_max2(abs_max2(abs_max2(m, b.x), b.y), b.z), b.w);
-        if (max(m & 0xFFFFu, m >> 16) >= 0x4780u) bad = 1;
-        const uint4 lo4 = make_uint4(bf16x2_to_f16x2(a.x), bf16x2_to_f16x2(a.z), bf16x2_to_f16x2(b.x),
-                                     bf16x2_to_f16x2(b.z));
-        const uint4 hi4 = make_uint4(bf16x2_to_f16x2(a.y), bf16x2_to_f16x2(a.w), bf16x2_to_f16x2(b.y),
-                                     bf16x2_to_f16x2(b.w));
-        uint8_t* const dst = Q + (g16 >> 2) * (SUB * 128) + row * 128;
-        const int c = 2 * (g16 & 3);
-        *reinterpret_cast<uint4*>(dst + ((c ^ (row & 7)) << 4)) = lo4;
-        *reinterpret_cast<uint4*>(dst + (((c + 1) ^ (row & 7)) << 4)) = hi4;
+        if (max(m & 0xFFFFu, m >> 16) >= 0x4780u) report(p.status, KVQ_DEV_RANGE);
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_addr(&S.q_full[h]));
-      named_sync(barid, 128);  // (also: the previous segment's epilogue has read ms)
-      if (tok < SUB) ms[tok] = 0.f;
-      if (has_tree) {
-        if (tok < p.N) S.anc[h][tok] = tree_ancestors(S.par[h], tok);
-        if (tok < 64) {
-          const uint32_t w = __ballot_sync(0xffffffffu, wild);
-          if (lane == 0) reinterpret_cast<uint32_t*>(&S.wild[h])[wq] = w;
-        }
-      }
-      named_sync(barid, 128);
+      if (lane == 0) mbar_arrive(smem_addr(&S.q_full));
+      named_sync(3, 256);
+      if (th < p.N && sg.blk1 > sg.nq + (sg.n_sink + sg.r) / kBlk) S.anc[th] = tree_ancestors(S.par, th);
+      named_sync(3, 256);
 
+      constexpr int kCh = 16;  // columns in registers at a time
       float l[SUB];
 #pragma unroll
       for (int j = 0; j < SUB; ++j) l[j] = 0.f;
       bool unset = true;  // some column has no maximum yet (uniform over the warpgroup)
       bool has = false;   // column `tok` has one
 
-      for (int blk = sg.blk0; blk < sg.blk1; ++blk, ++g) {
-        const bool first = blk == sg.blk0;
-        // which of the block's tokens count
+      const int blk0 = sg.blk0, blk1 = sg.blk1;
+#pragma unroll 1
+      for (int blk = blk0; blk < blk1; ++blk, ++g) {
+        const uint32_t sb = g & 1;
+        const uint32_t ts = tlane + Sh::kTmS + sb * NT + h * SUB, to = tlane + Sh::kTmO + h * SUB;
+        // ---- which of the half's columns see the thread's token ----
         const bool quant = blk < sg.nq;
-        bool valid = true, tree = false, spoilt = false;
-        unsigned long long desc = 0;
-        if (quant) {
-          const int x = blk * kBlk + tok;
-          valid = x < sg.ts.qn;
-          if (L.paged && valid) {
-            const int e = p.C.block_table[(long long)sg.b * L.mbps + x / L.P];
-            valid = e >= 0 && e < L.num_blocks;
-          }
-        } else {
-          const int nsr = sg.ts.n_sink + sg.ts.r;
-          const int x = (blk - sg.nq) * kBlk + tok;
-          valid = x < nsr;
-          tree = (blk - sg.nq) * kBlk + kBlk > nsr;  // (uniform) drafted nodes in this block
-          if (tree && !valid && x < nsr + p.N) {
-            for (int n = x - nsr; n < p.N; ++n) desc |= ((S.anc[h][n] >> (x - nsr)) & 1ull) << n;
-            spoilt = (S.wild[h] >> (x - nsr)) & 1ull;
-            valid = true;
-          } else if (valid) {
-            desc = ~0ull;
-          }
-        }
-        const float c = quant ? cq : p.scale_log2;
-        tree_wait(&S.s_full[h], (uint32_t)g & 1, abort, p.status);
-        tc_fence_after();
-        float x[SUB];
-#pragma unroll
-        for (int j = 0; j < SUB; j += 16) tc_ld16(ts_ + j, x + j);
-        tc_wait_ld();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&S.s_free[h]));
-        // x: the exponent (log2) relative to the column's maximum so far
-        float top = -INFINITY;
-#pragma unroll
-        for (int j = 0; j < SUB; j += 4) {
-          const float4 m4 = *reinterpret_cast<const float4*>(ms + j);
-          const float2 a = fma_f32x2(make_float2(x[j], x[j + 1]), make_float2(c, c), make_float2(-m4.x, -m4.y));
-          const float2 b = fma_f32x2(make_float2(x[j + 2], x[j + 3]), make_float2(c, c), make_float2(-m4.z, -m4.w));
-          x[j] = a.x;
-          x[j + 1] = a.y;
-          x[j + 2] = b.x;
-          x[j + 3] = b.y;
-        }
-        if (__any_sync(0xffffffffu, !valid || tree)) {
-          if (tree && valid) {
-            int n = col0 / p.gh, k = col0 - n * p.gh;
-#pragma unroll
-            for (int j = 0; j < SUB; ++j) {
-              if (n < 64) {
-                if (!((desc >> n) & 1ull)) x[j] = -INFINITY;
-                else if (spoilt) x[j] = NAN;
+        bool masked = false, spoilt = false;
+        unsigned long long allow = ~0ull;
+        if (!quant || L.paged || blk * kBlk + kBlk > sg.qn) {
+          bool valid;
+          if (quant) {
+            const int x = blk * kBlk + tok;
+            valid = x < sg.qn;
+            if (L.paged && valid) {
+              const int e = p.C.block_table[(long long)sg.b * L.mbps + x / L.P];
+              valid = e >= 0 && e < L.num_blocks;
+            }
+            allow = valid ? ~0ull : 0ull;
+          } else {
+            const int nsr = sg.n_sink + sg.r, x = (blk - sg.nq) * kBlk + tok;
+            valid = x < nsr;
+            if (!valid) allow = 0;
+            if (x >= nsr && x < nsr + p.N) {  // a drafted token: its descendants' columns
+              const int m = x - nsr;
+              spoilt = (S.wild >> m) & 1ull;
+              int n = (sg.ch * NT + h * SUB) / p.gh, k = sg.ch * NT + h * SUB - n * p.gh;
+              for (int j = 0; j < SUB; ++j) {
+                if (n < p.N && ((S.anc[n] >> m) & 1ull)) allow |= 1ull << j;
+                if (++k == p.gh) { k = 0; ++n; }
               }
-              if (++k == p.gh) { k = 0; ++n; }
             }
           }
-          if (!valid) {
-#pragma unroll
-            for (int j = 0; j < SUB; ++j) x[j] = -INFINITY;
-          }
+          masked = __any_sync(kAll, !valid);
         }
+        const float c = F::kFp8 && quant ? p.scale_log2 * *p.C.k_tscale : p.scale_log2;
+        tree_wait(&S.s_full[sb], (g >> 1) & 1, abort, p.status);
+        tc_fence_after();
+        // columns c0 .. of the scores: exponents (log2) relative to the columns' maxima so far
+        float x[kCh];
+        auto scores = [&](int c0) {
+          tc_ld16(ts + c0, x);
+          tc_wait_ld();
 #pragma unroll
-        for (int j = 0; j < SUB; ++j) top = fmaxf(top, x[j]);
-        const bool slow = named_any(barid, 128, unset || !(top <= 8.f));
-        // the product of the previous block has read P (and written O)
-        if (g > 0) tree_wait(&S.p_free[h], (uint32_t)(g - 1) & 1, abort, p.status);
-        if (slow) {
-          // new column maxima over the block's 128 tokens
+          for (int j = 0; j < kCh; j += 4) {
+            const float4 m4 = *reinterpret_cast<const float4*>(ms + c0 + j);
+            const float2 a = fma_f32x2(make_float2(x[j], x[j + 1]), make_float2(c, c), make_float2(-m4.x, -m4.y));
+            const float2 b = fma_f32x2(make_float2(x[j + 2], x[j + 3]), make_float2(c, c), make_float2(-m4.z, -m4.w));
+            x[j] = a.x;
+            x[j + 1] = a.y;
+            x[j + 2] = b.x;
+            x[j + 3] = b.y;
+          }
+          if (masked) {
+            const uint32_t w = (uint32_t)(allow >> c0);
 #pragma unroll
-          for (int j = 0; j < SUB; ++j) {
-            float v = x[j];
+            for (int j = 0; j < kCh; ++j) x[j] = (w >> j) & 1u ? (spoilt ? NAN : x[j]) : -INFINITY;
+          }
+        };
+        float top = -INFINITY;
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-            if (lane == 0) S.red[h][wq][j] = v;
+        for (int c0 = 0; c0 < SUB; c0 += kCh) {
+          scores(c0);
+#pragma unroll
+          for (int j = 0; j < kCh; j += 2) top = fmaxf(fmaxf(x[j], x[j + 1]), top);
+        }
+        if (named_any(barid, 128, unset || !(top <= 8.f))) {
+          // ---- new column maxima over the block's 128 tokens ----
+#pragma unroll 1
+          for (int c0 = 0; c0 < SUB; c0 += kCh) {
+            scores(c0);
+#pragma unroll
+            for (int j = 0; j < kCh; ++j) {
+              float v = x[j];
+#pragma unroll
+              for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
+              if (lane == 0) S.red[wq][h * SUB + c0 + j] = v;
+            }
           }
           named_sync(barid, 128);
           if (tok < SUB) {
+            const int j = h * SUB + tok;
             // d: the block's maximum relative to the column's so far; its first one is taken as it is
-            const float d = fmaxf(fmaxf(S.red[h][0][tok], S.red[h][1][tok]), fmaxf(S.red[h][2][tok], S.red[h][3][tok]));
+            const float d = fmaxf(fmaxf(S.red[0][j], S.red[1][j]), fmaxf(S.red[2][j], S.red[3][j]));
             float rise = fmaxf(d, 0.f);
             if (!has) {
               has = d != -INFINITY;
               rise = has ? d : 0.f;
             }
-            ms[tok] += rise;
-            S.rise[h][tok] = rise;
-            S.fall[h][tok] = exp2_approx(-rise);
+            S.m[j] += rise;
+            S.fall[j] = exp2_approx(-rise);
             if (!has) S.unset[h] = 1;
           }
           named_sync(barid, 128);
           unset = S.unset[h] != 0;
 #pragma unroll
           for (int j = 0; j < SUB; j += 4) {
-            const float4 d = *reinterpret_cast<const float4*>(&S.rise[h][j]);
-            const float4 f = *reinterpret_cast<const float4*>(&S.fall[h][j]);
-            x[j] -= d.x;
-            x[j + 1] -= d.y;
-            x[j + 2] -= d.z;
-            x[j + 3] -= d.w;
+            const float4 f = *reinterpret_cast<const float4*>(&S.fall[h * SUB + j]);
             l[j] = scaled(l[j], f.x);
             l[j + 1] = scaled(l[j + 1], f.y);
             l[j + 2] = scaled(l[j + 2], f.z);
             l[j + 3] = scaled(l[j + 3], f.w);
           }
-          if (!first) {  // what O holds so far
+          if (blk > blk0) {  // what O holds so far, behind the previous block's product
+            tree_wait(&S.p_free[(g - 1) & 1], ((g - 1) >> 1) & 1, abort, p.status);
             tc_fence_after();
 #pragma unroll 1
             for (int j0 = 0; j0 < SUB; j0 += 8) {
               float o[8];
-              tc_ld8(to_ + j0, o);
+              tc_ld8(to + j0, o);
               tc_wait_ld();
 #pragma unroll
-              for (int j = 0; j < 8; ++j) o[j] = scaled(o[j], S.fall[h][j0 + j]);
-              tc_st8(to_ + j0, o);
+              for (int j = 0; j < 8; ++j) o[j] = scaled(o[j], S.fall[h * SUB + j0 + j]);
+              tc_st8(to + j0, o);
             }
             tc_wait_st();
           }
-          named_sync(barid, 128);  // (rise, fall and unset have been read)
+          named_sync(barid, 128);  // (fall and unset have been read)
           if (tok == 0) S.unset[h] = 0;
         }
+        // ---- P, where the product that read its buffer last is done ----
+        if (g > 1) tree_wait(&S.p_free[sb], ((g >> 1) - 1) & 1, abort, p.status);
+        uint8_t* const P = Ps + sb * Sh::kPBytes + (NT == 128 ? h * (kBlk * 128) : 0);
 #pragma unroll
-        for (int j = 0; j < SUB; j += 8) {
-          uint32_t w[4];
-#pragma unroll
-          for (int i = 0; i < 8; i += 2) {
-            const float a = exp2_approx(x[j + i]), b = exp2_approx(x[j + i + 1]);
-            l[j + i] += a;
-            l[j + i + 1] += b;
-            w[i >> 1] = pack_f16(a, b);
+        for (int c0 = 0; c0 < SUB; c0 += kCh) {
+          scores(c0);
+          if (c0 + kCh == SUB) {  // the last read of S
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&S.s_free[sb]));
           }
-          const uint32_t at = (uint32_t)(tok * SUB * 2 + j * 2);
-          constexpr uint32_t kM = SUB == 64 ? 7 : (SUB == 32 ? 3 : 1);
-          *reinterpret_cast<uint4*>(P + (at ^ (((at >> 7) & kM) << 4))) = make_uint4(w[0], w[1], w[2], w[3]);
+#pragma unroll
+          for (int j = 0; j < kCh; j += 8) {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+              const float2 e = make_float2(exp2_approx(x[j + i]), exp2_approx(x[j + i + 1]));
+              const float2 n = add_f32x2(make_float2(l[c0 + j + i], l[c0 + j + i + 1]), e);
+              l[c0 + j + i] = n.x;
+              l[c0 + j + i + 1] = n.y;
+              w[i >> 1] = pack_f16(e.x, e.y);
+            }
+            const uint32_t at = (uint32_t)(tok * Sh::kPRow + (NT == 128 ? 0 : h * SUB * 2) + (c0 + j) * 2);
+            *reinterpret_cast<uint4*>(P + (at ^ (((at >> 7) & Sh::kPMask) << 4))) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&S.p_full[h]));
+        if (lane == 0) mbar_arrive(smem_addr(&S.p_full[sb]));
       }
 
       // ---- epilogue: column sums, then O ----
@@ -1036,42 +1135,45 @@ __global__ void __launch_bounds__(TreeShape<SUB>::kThreads, 1) tree_kernel(const
       for (int j = 0; j < SUB; ++j) {
         float v = l[j];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        if (lane == 0) S.red[h][wq][j] = v;
+        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+        if (lane == 0) S.red[wq][h * SUB + j] = v;
       }
-      tree_wait(&S.p_free[h], (uint32_t)(g - 1) & 1, abort, p.status);
+      tree_wait(&S.p_free[(g - 1) & 1], ((g - 1) >> 1) & 1, abort, p.status);
       tc_fence_after();
       named_sync(barid, 128);
       const bool whole = sg.blk0 == 0 && sg.blk1 == sg.nblk;
-      const int which = sg.blk0 > 0 ? 0 : 1;  // a cut item is the CTA's first (slot 0) or its last (slot 1)
-      const long long slotid = cta * 2 + which;
-      const int NT = 2 * SUB;
+      const float vunit = F::kFp8 ? *p.C.v_tscale * (FMT == KVQ_FMT_FP8_E5M2 ? 256.f : 1.f) : 1.f;
+      // a cut item is the CTA's first (place 0) or its last (place 1)
+      const long long place = ((long long)blockIdx.x * 2 + (sg.blk0 > 0 ? 0 : 1)) * NT;
+      if (tok < SUB) {
+        const int j = h * SUB + tok, col = sg.ch * NT + j;
+        const float sum = (S.red[0][j] + S.red[1][j]) + (S.red[2][j] + S.red[3][j]);
+        int row = -1;
+        if (col < p.gh * p.N) {
+          const int n = col / p.gh;
+          row = (sg.b * p.N + n) * p.Hq + sg.h * p.gh + (col - n * p.gh);
+          if (!whole) {
+            p.ws_ml[(place + j) * 2] = sum == 0.f ? -INFINITY : S.m[j];
+            p.ws_ml[(place + j) * 2 + 1] = sum;
+          } else if (p.lse) {
+            p.lse[row] = sum == 0.f ? -INFINITY : (S.m[j] + log2f(sum)) * 0.69314718055994531f;
+          }
+        }
+        S.row[j] = row;
+        S.fall[j] = sum == 0.f ? 0.f : vunit / sum;
+      }
+      named_sync(barid, 128);
 #pragma unroll 1
-      for (int j0 = 0; j0 < SUB; j0 += 16) {
-        float o[16];
-        tc_ld16(to_ + j0, o);
+      for (int j0 = 0; j0 < SUB; j0 += 8) {
+        float o[8];
+        tc_ld8(tlane + Sh::kTmO + h * SUB + j0, o);
         tc_wait_ld();
 #pragma unroll
-        for (int jj = 0; jj < 16; ++jj) {
-          const int j = j0 + jj, col = col0 + j;
-          const float sum = (S.red[h][0][j] + S.red[h][1][j]) + (S.red[h][2][j] + S.red[h][3][j]);
-          if (col < C) {
-            if (whole) {
-              const int n = col / p.gh, hh = col - n * p.gh;
-              const long long row = ((long long)sg.b * p.N + n) * p.Hq + (long long)sg.h * p.gh + hh;
-              const float v = sum == 0.f ? 0.f : o[jj] * (vunit / sum);
-              if (p.out_bf16) reinterpret_cast<__nv_bfloat16*>(p.out)[row * L.d + tok] = __float2bfloat16_rn(v);
-              else reinterpret_cast<float*>(p.out)[row * L.d + tok] = v;
-              if (p.lse && tok == 0)
-                p.lse[row] = sum == 0.f ? -INFINITY : (ms[j] + log2f(sum)) * 0.69314718055994531f;
-            } else {
-              p.ws_o[(slotid * NT + h * SUB + j) * L.d + tok] = o[jj];
-              if (tok == 0) {
-                p.ws_ml[(slotid * NT + h * SUB + j) * 2] = sum == 0.f ? -INFINITY : ms[j];
-                p.ws_ml[(slotid * NT + h * SUB + j) * 2 + 1] = sum;
-              }
-            }
-          }
+        for (int jj = 0; jj < 8; ++jj) {
+          const int j = h * SUB + j0 + jj, row = S.row[j];
+          if (row < 0) continue;
+          if (!whole) p.ws_o[(place + j) * L.d + tok] = o[jj];
+          else put_out(p, row, tok, S.fall[j] == 0.f ? 0.f : o[jj] * S.fall[j]);
         }
       }
       tc_fence_before();
@@ -1079,58 +1181,53 @@ __global__ void __launch_bounds__(TreeShape<SUB>::kThreads, 1) tree_kernel(const
         // ---- the last CTA to finish the item merges its parts, in CTA order ----
         __threadfence();
         named_sync(3, 256);
-        const long long a0 = sg.item0, a1 = sg.item0 + sg.nblk;
+        const unsigned U = S.units, W = S.ctas, a0 = sg.item0, a1 = a0 + (unsigned)sg.nblk;
         // the CTAs whose ranges meet [a0, a1)
-        long long c0 = a0 * W / U, c1 = (a1 - 1) * W / U;
-        while (U * (c0 + 1) / W <= a0) ++c0;
-        while (U * c0 / W > a0) --c0;
-        while (U * (c1 + 1) / W <= a1 - 1) ++c1;
-        while (U * c1 / W > a1 - 1) --c1;
-        unsigned* const ctr = p.counters + ((long long)sg.b * L.H + sg.h) * p.chunks + sg.ch;
-        if (h == 0 && tok == 0) {
+        unsigned c0 = (unsigned)((unsigned long long)a0 * W / U), c1 = (unsigned)((unsigned long long)(a1 - 1) * W / U);
+        while (tree_unit(U, W, c0 + 1) <= a0) ++c0;
+        while (tree_unit(U, W, c1 + 1) <= a1 - 1) ++c1;
+        if (th == 0) {
+          unsigned* const ctr = p.counters + ((long long)sg.b * L.H + sg.h) * p.chunks + sg.ch;
           const unsigned n = atomicAdd(ctr, 1u);
-          S.last = n + 1 == (unsigned)(c1 - c0 + 1);
+          S.last = n + 1 == c1 - c0 + 1;
           if (S.last) *ctr = 0u;
         }
         named_sync(3, 256);
         if (S.last) {
           __threadfence();
-          for (int j = 0; j < SUB; ++j) {
-            const int col = col0 + j;
-            if (col >= C) break;
+          const long long p0 = ((long long)c0 * 2 + (tree_unit(U, W, c0) > a0 ? 0 : 1)) * NT;  // (its first part)
+#pragma unroll 1
+          for (int j = h * SUB; j < h * SUB + SUB; ++j) {
+            const int row = S.row[j];
+            if (row < 0) continue;
             float m = -INFINITY, sum = 0.f, acc = 0.f;
-            for (long long cc = c0; cc <= c1; ++cc) {
-              const long long sl = (cc * 2 + (U * cc / W > a0 ? 0 : 1)) * NT + h * SUB + j;
+            for (unsigned cc = c0; cc <= c1; ++cc) {
+              const long long sl = (cc == c0 ? p0 : (long long)cc * 2 * NT) + j;
               const float mi = __ldcg(p.ws_ml + sl * 2), li = __ldcg(p.ws_ml + sl * 2 + 1);
-              if (mi == -INFINITY) continue;
               const float oi = __ldcg(p.ws_o + sl * L.d + tok);
+              if (mi == -INFINITY) continue;
               const float mn = fmaxf(m, mi);
               const float fa = m == -INFINITY ? 0.f : exp2_approx(m - mn), fb = exp2_approx(mi - mn);
               sum = sum * fa + li * fb;
               acc = acc * fa + oi * fb;
               m = mn;
             }
-            const int n = col / p.gh, hh = col - n * p.gh;
-            const long long row = ((long long)sg.b * p.N + n) * p.Hq + (long long)sg.h * p.gh + hh;
-            const float v = sum == 0.f ? 0.f : acc * (vunit / sum);
-            if (p.out_bf16) reinterpret_cast<__nv_bfloat16*>(p.out)[row * L.d + tok] = __float2bfloat16_rn(v);
-            else reinterpret_cast<float*>(p.out)[row * L.d + tok] = v;
+            put_out(p, row, tok, sum == 0.f ? 0.f : acc * (vunit / sum));
             if (p.lse && tok == 0)
               p.lse[row] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.69314718055994531f;
           }
         }
       }
     }
-    if (bad) report(p.status, KVQ_DEV_RANGE);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == Sh::kDq + 8) tc_dealloc512(tm);
+  if (warp == 17) tc_dealloc512(tm);
 }
 
-template <int FMT, int SUB>
-cudaError_t launch_tree_sub(const TreeParams& p, int ctas, int smem, cudaStream_t stream) {
+template <int FMT, int NT>
+cudaError_t launch_tree_nt(const TreeParams& p, int ctas, int smem, cudaStream_t stream) {
   static std::mutex mu;
   static int set_for[64] = {};
   int dev = 0;
@@ -1139,24 +1236,24 @@ cudaError_t launch_tree_sub(const TreeParams& p, int ctas, int smem, cudaStream_
   {
     std::lock_guard<std::mutex> lock(mu);
     if (dev < 0 || dev >= 64 || set_for[dev] < smem) {
-      e = cudaFuncSetAttribute(tree_kernel<FMT, SUB>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      e = cudaFuncSetAttribute(tree_kernel<FMT, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
       if (e != cudaSuccess) return e;
       cudaFuncAttributes fa;  // the register split draws on what the launch brings
-      e = cudaFuncGetAttributes(&fa, tree_kernel<FMT, SUB>);
+      e = cudaFuncGetAttributes(&fa, tree_kernel<FMT, NT>);
       if (e != cudaSuccess) return e;
-      if (fa.numRegs < TreeShape<SUB>::kRegLaunch) return cudaErrorInvalidConfiguration;
+      if (fa.numRegs < TreeShape<NT>::kRegLaunch) return cudaErrorInvalidConfiguration;
       if (dev >= 0 && dev < 64) set_for[dev] = smem;
     }
   }
-  return launch_pdl(tree_kernel<FMT, SUB>, dim3(ctas), dim3(TreeShape<SUB>::kThreads), (size_t)smem, stream, p);
+  return launch_pdl(tree_kernel<FMT, NT>, dim3(ctas), dim3(TreeShape<NT>::kThreads), (size_t)smem, stream, p);
 }
 
 template <int FMT>
-cudaError_t launch_tree_fmt(const TreeParams& p, int sub, int ctas, int smem, cudaStream_t stream) {
-  switch (sub) {
-    case 16: return launch_tree_sub<FMT, 16>(p, ctas, smem, stream);
-    case 32: return launch_tree_sub<FMT, 32>(p, ctas, smem, stream);
-    default: return launch_tree_sub<FMT, 64>(p, ctas, smem, stream);
+cudaError_t launch_tree_fmt(const TreeParams& p, int nt, int ctas, int smem, cudaStream_t stream) {
+  switch (nt) {
+    case 32: return launch_tree_nt<FMT, 32>(p, ctas, smem, stream);
+    case 64: return launch_tree_nt<FMT, 64>(p, ctas, smem, stream);
+    default: return launch_tree_nt<FMT, 128>(p, ctas, smem, stream);
   }
 }
 

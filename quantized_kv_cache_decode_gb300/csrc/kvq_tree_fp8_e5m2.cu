@@ -3,8 +3,8 @@
 
 namespace kvq {
 
-cudaError_t launch_tree_fp8_e5m2(const TreeParams& p, int sub, int ctas, int smem, cudaStream_t stream) {
-  return launch_tree_fmt<KVQ_FMT_FP8_E5M2>(p, sub, ctas, smem, stream);
+cudaError_t launch_tree_fp8_e5m2(const TreeParams& p, int nt, int ctas, int smem, cudaStream_t stream) {
+  return launch_tree_fmt<KVQ_FMT_FP8_E5M2>(p, nt, ctas, smem, stream);
 }
 
 }  // namespace kvq
