@@ -130,8 +130,13 @@ struct TreeParams {
   float* lse;
 };
 
-// CTAs that share a tree launch's blocks: all of them, at least one block each
-__host__ __device__ inline long long tree_ctas(long long grid, long long blocks) {
+// CTAs that share a tree launch's blocks: whole items each where all are of one length and fill at
+// least 80 % of the grid that way (nothing is cut and merged), else all CTAs, at least one block each.
+__host__ __device__ inline long long tree_ctas(long long grid, long long blocks, long long items, bool equal) {
+  if (equal && items > 0) {
+    const long long k = (items + grid - 1) / grid;
+    if (items % k == 0 && (items / k) * 5 >= grid * 4) return items / k;
+  }
   return blocks < grid ? (blocks < 1 ? 1 : blocks) : grid;
 }
 constexpr int kMaxNodes = 64;  // nodes of a tree: one bit each in the ancestor masks

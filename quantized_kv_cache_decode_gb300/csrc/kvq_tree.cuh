@@ -125,6 +125,11 @@ __device__ __forceinline__ float2 add_f32x2(float2 a, float2 b) {
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;
 }
+__device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
 // one lane of the warp
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
@@ -190,7 +195,7 @@ struct TreeCursor {
 };
 
 struct TreeSmem {  // small shared state, after the big buffers
-  unsigned long long slot_full[kMaxSlots], slot_empty[kMaxSlots];
+  unsigned long long slot_full[kMaxSlots], slot_ready[kMaxSlots], slot_empty[kMaxSlots];
   unsigned long long k_full[2], k_empty[2], v_full[2], v_empty[2];
   unsigned long long s_full[2], s_free[2], p_full[2], p_free[2], q_full, drain;
   uint32_t slot_ok[kMaxSlots];  // quantized slots: which of the four tiles were copied
@@ -206,6 +211,8 @@ struct TreeSmem {  // small shared state, after the big buffers
   unsigned long long wild;        // nodes whose drafted Values f16 does not hold
   int par[64];
   unsigned units, ctas;           // blocks of the launch, CTAs that share them
+  float kscale, vunit;            // FP8: the Keys' tensor scale, the unit of the Values (else 1)
+  int least, most;                // blocks of the shortest and the longest sequence
   TreeCursor cur[20];             // per warp
   TreeSeg seg[20];
 };
@@ -287,31 +294,6 @@ __device__ __forceinline__ bool tree_wait(unsigned long long* bar, uint32_t pari
 // ---------------------------------------------------------------------------
 // dequantization of 16-token tiles to f16 operand fragments
 // ---------------------------------------------------------------------------
-// the code at bit OFF (< 23 - BITS) of w, exact in fp32: placed in the mantissa of 2^23, then
-// (2^23 + code 2^OFF) 2^-OFF - 2^(23-OFF) in one exact fma
-template <int BITS, int OFF>
-__device__ __forceinline__ float2 codes_f32(uint32_t lo, uint32_t hi) {
-  constexpr uint32_t kMask = ((1u << BITS) - 1u) << OFF;
-  constexpr float kMul = 1.0f / (float)(1u << OFF), kAdd = -8388608.0f / (float)(1u << OFF);
-  const float a = __uint_as_float(lop3_and_or(lo, kMask, 0x4B000000u));
-  const float b = __uint_as_float(lop3_and_or(hi, kMask, 0x4B000000u));
-  return fma_f32x2(make_float2(a, b), make_float2(kMul, kMul), make_float2(kAdd, kAdd));
-}
-
-// the code pair (half 0, half 1) of register REG of step s's fragment; w: the lane's operand words
-template <int FMT, int REG>
-__device__ __forceinline__ float2 frag_codes(const uint32_t* w, int s) {
-  if constexpr (FMT == KVQ_FMT_INT4) {
-    return codes_f32<4, 4 * REG>(w[s], w[s] >> 16);
-  } else if constexpr (FMT == KVQ_FMT_INT2) {
-    const uint32_t x = w[s >> 1];
-    return (s & 1) ? codes_f32<2, 8 + 2 * REG>(x, x >> 16) : codes_f32<2, 2 * REG>(x, x >> 16);
-  } else {
-    const uint32_t x = w[2 * s + (REG >> 1)];
-    return codes_f32<8, 0>(x >> (8 * (REG & 1)), x >> (8 * (REG & 1) + 16));
-  }
-}
-
 template <int FMT>
 struct TreeFmt {
   static constexpr bool kFp8 = FMT == KVQ_FMT_FP8_E4M3 || FMT == KVQ_FMT_FP8_E5M2;
@@ -326,9 +308,34 @@ __device__ __forceinline__ void fp8_pairs(uint32_t w, uint32_t& a, uint32_t& b) 
   else e4m3x4_to_f16x4(w, a, b);
 }
 
+// Integer codes n as n - 2^(b-1), a pair per register, exact: placed in the mantissa of 1024
+// (1024 + n 2^o, one ulp is 1), then one fma takes the 2^o and the offset out.  Register REG of step s.
+template <int FMT, int REG>
+__device__ __forceinline__ uint32_t centred(const uint32_t* w, int s) {
+  constexpr uint32_t kMagic = 0x64006400u;  // 1024, 1024
+  uint32_t x;
+  if constexpr (FMT == KVQ_FMT_INT8) {  // bytes (REG & 1), (REG & 1) + 2 of word 2s + REG / 2
+    x = __byte_perm(w[2 * s + (REG >> 1)], kMagic, (REG & 1) ? 0x7351 : 0x7250);
+    return hadd2(x, 0xE480E480u);  // - 1152
+  } else if constexpr (FMT == KVQ_FMT_INT4) {  // bits 4 REG, 4 REG + 16 of word s
+    x = (REG >> 1) ? w[s] >> 8 : w[s];
+    if constexpr ((REG & 1) == 0) return hadd2(lop3_and_or(x, 0x000F000Fu, kMagic), 0xE408E408u);  // - 1032
+    else return hfma2(lop3_and_or(x, 0x00F000F0u, kMagic), 0x2C002C00u, 0xD480D480u);               // / 16 - 72
+  } else {  // bits 8 (s & 1) + 2 REG, + 16 of word s / 2
+    x = w[s >> 1] >> (8 * (s & 1));
+    constexpr uint32_t kMul[4] = {0x3C003C00u, 0x34003400u, 0x2C002C00u, 0x24002400u};  // 2^-2REG
+    constexpr uint32_t kAdd[4] = {0xE402E402u, 0xDC08DC08u, 0xD420D420u, 0xCC80CC80u};  // -(2^(10 - 2REG) + 2)
+    return hfma2(lop3_and_or(x, 0x00030003u << (2 * REG), kMagic), kMul[REG], kAdd[REG]);
+  }
+}
+
+// Scales as the dequantization reads them (f16 pairs, written over the fp32 ones by the prep warps): a value is
+// s m + c with m the centred code and c = s (2^(b-1) - z).  K: 16 bytes per four channels {s01, s23, c01, c23};
+// V: per group of channels, 16 bytes per q {s of tokens 2q, 2q+1; of 2q+8, 2q+9; c of both}.
+
 // K fragments of steps 4i .. 4i+3 of a tile (rows = tokens; register pairs = channels 16s + 4q + {0,1}, {2,3})
 template <int FMT>
-__device__ __forceinline__ void k_frags(const uint32_t* w, const float* hdr, int i, int q, uint32_t (&r)[16]) {
+__device__ __forceinline__ void k_frags(const uint32_t* w, const uint8_t* hdr, int i, int q, uint32_t (&r)[16]) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const int s = 4 * i + j;
@@ -336,23 +343,18 @@ __device__ __forceinline__ void k_frags(const uint32_t* w, const float* hdr, int
       fp8_pairs<FMT>(w[2 * s], r[4 * j], r[4 * j + 1]);
       fp8_pairs<FMT>(w[2 * s + 1], r[4 * j + 2], r[4 * j + 3]);
     } else {
-      const float4 sc = *reinterpret_cast<const float4*>(hdr + 16 * s + 4 * q);
-      const float4 z = *reinterpret_cast<const float4*>(hdr + 128 + 16 * s + 4 * q);
-      const float2 s01 = make_float2(sc.x, sc.y), s23 = make_float2(sc.z, sc.w);
-      const float2 n01 = make_float2(-sc.x * z.x, -sc.y * z.y), n23 = make_float2(-sc.z * z.z, -sc.w * z.w);
-      const float2 a = fma_f32x2(frag_codes<FMT, 0>(w, s), s01, n01), b = fma_f32x2(frag_codes<FMT, 1>(w, s), s01, n01);
-      const float2 c = fma_f32x2(frag_codes<FMT, 2>(w, s), s23, n23), d = fma_f32x2(frag_codes<FMT, 3>(w, s), s23, n23);
-      r[4 * j] = pack_f16(a.x, a.y);
-      r[4 * j + 1] = pack_f16(b.x, b.y);
-      r[4 * j + 2] = pack_f16(c.x, c.y);
-      r[4 * j + 3] = pack_f16(d.x, d.y);
+      const uint4 sc = *reinterpret_cast<const uint4*>(hdr + (4 * s + q) * 16);
+      r[4 * j] = hfma2(centred<FMT, 0>(w, s), sc.x, sc.z);
+      r[4 * j + 1] = hfma2(centred<FMT, 1>(w, s), sc.x, sc.z);
+      r[4 * j + 2] = hfma2(centred<FMT, 2>(w, s), sc.y, sc.w);
+      r[4 * j + 3] = hfma2(centred<FMT, 3>(w, s), sc.y, sc.w);
     }
   }
 }
 
 // V^T fragment of step s (rows = channels 16s + .., register pairs = tokens 2q + {0,1}, then + 8)
 template <int FMT>
-__device__ __forceinline__ void v_frag(const uint32_t* w, int s, float4 sc, float4 nz, uint32_t* r) {
+__device__ __forceinline__ void v_frag(const uint32_t* w, int s, const uint4& sc, uint32_t* r) {
   if constexpr (TreeFmt<FMT>::kFp8) {
     fp8_pairs<FMT>(w[2 * s], r[0], r[1]);
     fp8_pairs<FMT>(w[2 * s + 1], r[2], r[3]);
@@ -361,14 +363,10 @@ __device__ __forceinline__ void v_frag(const uint32_t* w, int s, float4 sc, floa
       for (int i = 0; i < 4; ++i) r[i] = hfma2(r[i], 0x1C001C00u, 0x80008000u);
     }
   } else {
-    const float2 s01 = make_float2(sc.x, sc.y), s23 = make_float2(sc.z, sc.w);
-    const float2 n01 = make_float2(nz.x, nz.y), n23 = make_float2(nz.z, nz.w);
-    const float2 a = fma_f32x2(frag_codes<FMT, 0>(w, s), s01, n01), b = fma_f32x2(frag_codes<FMT, 1>(w, s), s01, n01);
-    const float2 c = fma_f32x2(frag_codes<FMT, 2>(w, s), s23, n23), d = fma_f32x2(frag_codes<FMT, 3>(w, s), s23, n23);
-    r[0] = pack_f16(a.x, a.y);
-    r[1] = pack_f16(b.x, b.y);
-    r[2] = pack_f16(c.x, c.y);
-    r[3] = pack_f16(d.x, d.y);
+    r[0] = hfma2(centred<FMT, 0>(w, s), sc.x, sc.z);
+    r[1] = hfma2(centred<FMT, 1>(w, s), sc.x, sc.z);
+    r[2] = hfma2(centred<FMT, 2>(w, s), sc.y, sc.w);
+    r[3] = hfma2(centred<FMT, 3>(w, s), sc.y, sc.w);
   }
 }
 
@@ -385,22 +383,6 @@ __device__ __forceinline__ void load_words(const uint8_t* codes, int lane, uint3
   }
 }
 
-// scales s and -s z of a tile's Values, group j, for the tokens 2q, 2q + 1, 2q + 8, 2q + 9
-__device__ __forceinline__ void value_scales(const float* vs, int ngv, int j, int q, float4& sc, float4& nz) {
-  const float* vz = vs + 16 * ngv;
-  float4 z;
-  if (ngv == 1) {
-    const float2 a = *reinterpret_cast<const float2*>(vs + 2 * q), b = *reinterpret_cast<const float2*>(vs + 2 * q + 8);
-    const float2 c = *reinterpret_cast<const float2*>(vz + 2 * q), d = *reinterpret_cast<const float2*>(vz + 2 * q + 8);
-    sc = make_float4(a.x, a.y, b.x, b.y);
-    z = make_float4(c.x, c.y, d.x, d.y);
-  } else {
-    const int i0 = 2 * q * ngv + j, i1 = i0 + ngv, i2 = i0 + 8 * ngv, i3 = i2 + ngv;
-    sc = make_float4(vs[i0], vs[i1], vs[i2], vs[i3]);
-    z = make_float4(vz[i0], vz[i1], vz[i2], vz[i3]);
-  }
-  nz = make_float4(-sc.x * z.x, -sc.y * z.y, -sc.z * z.z, -sc.w * z.w);
-}
 // largest magnitude that a group of scale s and zero point z stands for
 __device__ __forceinline__ float group_reach(float s, float z, float levels) {
   return fabsf(s) * fmaxf(fabsf(z), fabsf(levels - z));
@@ -455,7 +437,8 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
   if (tid == 0) {
     for (int i = 0; i < kMaxSlots; ++i) {
       mbar_init(smem_addr(&S.slot_full[i]), 32);
-      mbar_init(smem_addr(&S.slot_empty[i]), F::kFp8 ? 8 : 9);
+      mbar_init(smem_addr(&S.slot_ready[i]), 1);
+      mbar_init(smem_addr(&S.slot_empty[i]), 8);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_addr(&S.k_full[i]), 4);
@@ -479,6 +462,10 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
   }
   pdl_wait();
   pdl_trigger();
+  if (tid == 0) {
+    S.kscale = F::kFp8 ? *p.C.k_tscale : 1.f;
+    S.vunit = F::kFp8 ? *p.C.v_tscale * (FMT == KVQ_FMT_FP8_E5M2 ? 256.f : 1.f) : 1.f;
+  }
   for (int b = tid; b < p.batch; b += Sh::kThreads) {
     long long T = p.seq_lens[b];
     const long long cap = max_tokens(L);
@@ -493,11 +480,12 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
   }
   __syncthreads();
   if (warp == 0) {
-    int run = 0;
+    int run = 0, least = 0x7FFFFFFF, most = 0;
     if (lane == 0) pre[0] = 0;
 #pragma unroll 1
     for (int b0 = 0; b0 < p.batch; b0 += 32) {
       int v = b0 + lane < p.batch ? pre[b0 + lane + 1] : 0;
+      if (b0 + lane < p.batch) least = min(least, v), most = max(most, v);
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int x = __shfl_up_sync(kAll, v, o);
@@ -506,6 +494,9 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
       if (b0 + lane < p.batch) pre[b0 + lane + 1] = run + v;
       run += __shfl_sync(kAll, v, 31);
     }
+    least = __reduce_min_sync(kAll, least);
+    most = __reduce_max_sync(kAll, most);
+    if (lane == 0) S.least = least, S.most = most;
   }
   tc_fence_before();
   __syncthreads();
@@ -515,7 +506,7 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
   TreeCursor& cur = S.cur[warp];
   TreeSeg& sg = S.seg[warp];
   if (lane == 0) {
-    const unsigned U = (unsigned)pre[p.batch] * (unsigned)(L.H * p.chunks), W = (unsigned)tree_ctas(gridDim.x, U);
+    const unsigned U = (unsigned)pre[p.batch] * (unsigned)(L.H * p.chunks), W = (unsigned)tree_ctas(gridDim.x, U, (long long)p.batch * L.H * p.chunks, S.least == S.most);
     S.units = U;
     S.ctas = W;
     const unsigned c = blockIdx.x;
@@ -681,39 +672,73 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
         mbar_wait_bounded(smem_addr(&S.drain), 0, kTreeWait);
       }
       __syncwarp();
-    } else if (!F::kFp8 && warp == 18) {
-      // ======================= check: scales that leave f16 =======================
-      // a group's values are s (n - z) with n in [0, L]
-      constexpr float kL = (float)((1 << F::kBits) - 1);
+    } else if (!F::kFp8) {
+      // ======================= prep: scales to f16, two warps in turn =======================
+      constexpr float kL = (float)((1 << F::kBits) - 1), kHalf = (float)(1 << (F::kBits - 1));
       int slot = 0;
-      uint32_t ph = 0;
+      uint32_t ph = 0, n = 0;
       bool ok = true;
-      float worst = 0.f;
+      float worst = 0.f;  // largest magnitude that any group stands for
+      const int ngv = L.ngv, lg = 31 - __clz(ngv);
       while (ok && tree_next(p, pre, lens, cur, sg)) {
         const int blk1 = sg.blk1, nq = sg.nq;
         for (int blk = sg.blk0; ok && blk < blk1; ++blk) {
           const bool quant = blk < nq;
-          const int n = quant ? 2 : kBlk / p.bf_tokens;
-          for (int i = 0; i < n; ++i) {
-            if (!(ok = tree_wait(&S.slot_full[slot], ph, abort, p.status))) break;
-            const uint32_t okmask = S.slot_ok[slot];
-            if (quant) {
-              const uint8_t* const src = slots + (size_t)slot * p.slot_bytes;
-              const int t0 = blk * 8 + i * 4;
-              for (int ti = 0; ti < 4; ++ti) {
-                if (!((okmask >> ti) & 1u)) continue;
-                if (ti == 0 || (t0 + ti) % L.tpg == 0) {
-                  const float* hdr = reinterpret_cast<const float*>(src + ((t0 + ti) / L.tpg - t0 / L.tpg) * 1024);
-#pragma unroll
-                  for (int c = 0; c < 128; c += 32) worst = fmaxf(worst, group_reach(hdr[c + lane], hdr[128 + c + lane], kL));
+          const int parts = quant ? 2 : kBlk / p.bf_tokens;
+          for (int i = 0; i < parts; ++i, ++n) {
+            if ((n & 1) == (uint32_t)(warp & 1)) {
+              if (!(ok = tree_wait(&S.slot_full[slot], ph, abort, p.status))) break;
+              if (quant) {
+                const uint32_t okmask = S.slot_ok[slot];
+                uint8_t* const src = slots + (size_t)slot * p.slot_bytes;
+                const int t0 = blk * 8 + i * 4, r0 = t0 / L.tpg;
+                const int last = 31 - __clz(okmask | 1u), nh = (t0 + last) / L.tpg - r0 + 1;
+                for (int e = 0; e < nh; ++e) {  // (a header whose tiles were not copied holds anything, and is not used)
+                  const float4 sc = reinterpret_cast<const float4*>(src + e * 1024)[lane];
+                  const float4 z = reinterpret_cast<const float4*>(src + e * 1024 + 512)[lane];
+                  const float top = fmaxf(fmaxf(group_reach(sc.x, z.x, kL), group_reach(sc.y, z.y, kL)),
+                                          fmaxf(group_reach(sc.z, z.z, kL), group_reach(sc.w, z.w, kL)));
+                  // (its first tile of the slot)
+                  const int ti = e == 0 ? 0 : (r0 + e) * L.tpg - t0;
+                  if ((okmask >> ti) & 1u) worst = fmaxf(worst, top);
+                  __syncwarp();
+                  reinterpret_cast<uint4*>(src + e * 1024)[lane] = make_uint4(
+                      pack_f16(sc.x, sc.y), pack_f16(sc.z, sc.w),
+                      pack_f16(sc.x * (kHalf - z.x), sc.y * (kHalf - z.y)),
+                      pack_f16(sc.z * (kHalf - z.z), sc.w * (kHalf - z.w)));
                 }
-                const float* vs =
-                    reinterpret_cast<const float*>(src + p.slot_hdr + ti * L.tile_bytes + 32 * F::kRb);
-                for (int c = lane; c < 16 * L.ngv; c += 32) worst = fmaxf(worst, group_reach(vs[c], vs[16 * L.ngv + c], kL));
+                // Values: token pairs of a tile and group, 8 ngv per tile; up to 64 (whole tiles) at a time
+#pragma unroll 1
+                for (int at0 = 0; at0 < 32 * ngv; at0 += 64) {
+                  float2 sv[2], zv[2];
+                  uint32_t* to[2];
+#pragma unroll
+                  for (int k = 0; k < 2; ++k) {
+                    const int at = at0 + k * 32 + lane, ti = at >> (3 + lg), within = at & (8 * ngv - 1);
+                    const int pr = within >> lg, j = within & (ngv - 1);  // tokens 2 pr, 2 pr + 1 of group j
+                    uint8_t* const vs = src + p.slot_hdr + ti * L.tile_bytes + 32 * F::kRb;
+                    to[k] = nullptr;
+                    if (ti < 4 && ((okmask >> ti) & 1u)) {
+                      const float* f = reinterpret_cast<const float*>(vs) + 2 * pr * ngv + j;
+                      sv[k] = make_float2(f[0], f[ngv]);
+                      zv[k] = make_float2(f[16 * ngv], f[17 * ngv]);
+                      to[k] = reinterpret_cast<uint32_t*>(vs) + j * 16 + (pr & 3) * 4 + (pr >> 2);
+                    }
+                  }
+                  __syncwarp();
+#pragma unroll
+                  for (int k = 0; k < 2; ++k) {
+                    if (to[k]) {
+                      worst = fmaxf(worst, fmaxf(group_reach(sv[k].x, zv[k].x, kL), group_reach(sv[k].y, zv[k].y, kL)));
+                      to[k][0] = pack_f16(sv[k].x, sv[k].y);
+                      to[k][2] = pack_f16(sv[k].x * (kHalf - zv[k].x), sv[k].y * (kHalf - zv[k].y));
+                    }
+                  }
+                }
               }
+              __syncwarp();
+              if (lane == 0) mbar_arrive(smem_addr(&S.slot_ready[slot]));
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_addr(&S.slot_empty[slot]));
             if (++slot == p.nslots) { slot = 0; ph ^= 1; }
           }
         }
@@ -729,6 +754,7 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
     const uint32_t tlane = tm + ((uint32_t)(32 * wq) << 16) + (isV ? Sh::kTmV : Sh::kTmK);
     unsigned long long* const full = isV ? S.v_full : S.k_full;
     unsigned long long* const empty = isV ? S.v_empty : S.k_empty;
+    unsigned long long* const ready = F::kFp8 ? S.slot_full : S.slot_ready;
     int slot = 0;
     uint32_t ph = 0, g = 0;
     bool ok = true, bad = false;
@@ -744,7 +770,7 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
         if (blk < nq) {
 #pragma unroll 1
           for (int half = 0; half < 2; ++half) {
-            if (!(ok = tree_wait(&S.slot_full[slot], ph, abort, p.status))) break;
+            if (!(ok = tree_wait(&ready[slot], ph, abort, p.status))) break;
             const uint8_t* const src = slots + (size_t)slot * p.slot_bytes;
             const uint32_t okmask = S.slot_ok[slot];
             const int t0 = blk * 8 + half * 4;
@@ -754,9 +780,7 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
                 for (int e = 0; e < 2; ++e) {
                   const int ti = 2 * (wq & 1) + e;  // tile of the slot
                   if (!((okmask >> ti) & 1u)) continue;
-                  const float* hdr = nullptr;
-                  if constexpr (!F::kFp8)
-                    hdr = reinterpret_cast<const float*>(src + ((t0 + ti) / L.tpg - t0 / L.tpg) * 1024);
+                  const uint8_t* const hdr = F::kFp8 ? src : src + ((t0 + ti) / L.tpg - t0 / L.tpg) * 1024;
                   uint32_t w[F::kWords];
                   load_words<FMT>(src + p.slot_hdr + ti * L.tile_bytes, lane, w);
 #pragma unroll
@@ -768,7 +792,7 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
                 }
               }
             } else {
-              const int ngv = F::kFp8 ? 1 : L.ngv;
+              const int g0 = F::kFp8 ? 0 : 32 * wq / L.Gv, g1 = F::kFp8 ? 0 : (32 * wq + 16) / L.Gv;
 #pragma unroll 1
               for (int tp = 0; tp < 4; tp += 2) {  // two tiles, channels 32 wq .. and 32 wq + 16 ..
                 uint32_t f[2][8];
@@ -793,13 +817,13 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
                       w[0] = *reinterpret_cast<const uint32_t*>(codes + lane * 16 + wq * 4);
                       w[1] = w[0] >> 8;
                     }
-                    float4 sc = make_float4(1.f, 1.f, 1.f, 1.f), nz = make_float4(0.f, 0.f, 0.f, 0.f);
-                    const float* const vs = reinterpret_cast<const float*>(tile + 32 * F::kRb);
-                    if constexpr (!F::kFp8) value_scales(vs, ngv, (32 * wq) / L.Gv, q, sc, nz);
-                    v_frag<FMT>(w, 0, sc, nz, f[0] + 4 * u);
-                    if constexpr (!F::kFp8)
-                      if (L.Gv == 16) value_scales(vs, ngv, 2 * wq + 1, q, sc, nz);
-                    v_frag<FMT>(w + (F::kBits == 8 ? 2 : 1), 0, sc, nz, f[1] + 4 * u);
+                    uint4 s0 = make_uint4(0, 0, 0, 0), s1 = s0;  // scales of the two steps' channels
+                    if constexpr (!F::kFp8) {
+                      s0 = *reinterpret_cast<const uint4*>(tile + 32 * F::kRb + g0 * 64 + q * 16);
+                      s1 = *reinterpret_cast<const uint4*>(tile + 32 * F::kRb + g1 * 64 + q * 16);
+                    }
+                    v_frag<FMT>(w, 0, s0, f[0] + 4 * u);
+                    v_frag<FMT>(w + (F::kBits == 8 ? 2 : 1), 0, s1, f[1] + 4 * u);
                     if constexpr (F::kFp8) {
                       // tokens behind the last one of a partly filled tile: zeros whatever the store holds
                       const int nv = sg.qn - 16 * (t0 + ti);
@@ -826,10 +850,10 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
         } else {
           uint32_t top = 0;
           const bool drafts = (blk - nq) * kBlk + kBlk > sg.n_sink + sg.r;
-          const float vinv = F::kFp8 && isV ? 1.f / (*p.C.v_tscale * (FMT == KVQ_FMT_FP8_E5M2 ? 256.f : 1.f)) : 1.f;
+          const float vinv = F::kFp8 && isV ? 1.f / S.vunit : 1.f;
 #pragma unroll 1
           for (int part = 0; part < kBlk; part += p.bf_tokens) {
-            if (!(ok = tree_wait(&S.slot_full[slot], ph, abort, p.status))) break;
+            if (!(ok = tree_wait(&ready[slot], ph, abort, p.status))) break;
             const uint8_t* const src = slots + (size_t)slot * p.slot_bytes;
             if (!isV) {
               if (32 * wq >= part && 32 * wq < part + p.bf_tokens) {
@@ -923,7 +947,7 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
             up = -1;
           }
           S.par[th] = up;
-          const float vinv = F::kFp8 ? 1.f / (*p.C.v_tscale * (FMT == KVQ_FMT_FP8_E5M2 ? 256.f : 1.f)) : 1.f;
+          const float vinv = F::kFp8 ? 1.f / S.vunit : 1.f;
           const uint4* v = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.v_draft) +
                                                           (((long long)sg.b * L.H + sg.h) * p.N + th) * L.d);
           uint32_t m = 0;
@@ -971,7 +995,7 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
       if (th < p.N && sg.blk1 > sg.nq + (sg.n_sink + sg.r) / kBlk) S.anc[th] = tree_ancestors(S.par, th);
       named_sync(3, 256);
 
-      constexpr int kCh = 16;  // columns in registers at a time
+      constexpr int kCh = SUB == 64 ? 16 : SUB;  // columns in registers at a time
       float l[SUB];
 #pragma unroll
       for (int j = 0; j < SUB; ++j) l[j] = 0.f;
@@ -1013,13 +1037,14 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
           }
           masked = __any_sync(kAll, !valid);
         }
-        const float c = F::kFp8 && quant ? p.scale_log2 * *p.C.k_tscale : p.scale_log2;
+        const float c = F::kFp8 && quant ? p.scale_log2 * S.kscale : p.scale_log2;
         tree_wait(&S.s_full[sb], (g >> 1) & 1, abort, p.status);
         tc_fence_after();
         // columns c0 .. of the scores: exponents (log2) relative to the columns' maxima so far
         float x[kCh];
         auto scores = [&](int c0) {
-          tc_ld16(ts + c0, x);
+#pragma unroll
+          for (int j = 0; j < kCh; j += 16) tc_ld16(ts + c0 + j, x + j);
           tc_wait_ld();
 #pragma unroll
           for (int j = 0; j < kCh; j += 4) {
@@ -1097,13 +1122,14 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
           }
           named_sync(barid, 128);  // (fall and unset have been read)
           if (tok == 0) S.unset[h] = 0;
+          if (kCh == SUB) scores(0);
         }
         // ---- P, where the product that read its buffer last is done ----
         if (g > 1) tree_wait(&S.p_free[sb], ((g >> 1) - 1) & 1, abort, p.status);
         uint8_t* const P = Ps + sb * Sh::kPBytes + (NT == 128 ? h * (kBlk * 128) : 0);
 #pragma unroll
         for (int c0 = 0; c0 < SUB; c0 += kCh) {
-          scores(c0);
+          if (kCh < SUB) scores(c0);
           if (c0 + kCh == SUB) {  // the last read of S
             tc_fence_before();
             __syncwarp();
@@ -1142,7 +1168,7 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
       tc_fence_after();
       named_sync(barid, 128);
       const bool whole = sg.blk0 == 0 && sg.blk1 == sg.nblk;
-      const float vunit = F::kFp8 ? *p.C.v_tscale * (FMT == KVQ_FMT_FP8_E5M2 ? 256.f : 1.f) : 1.f;
+      const float vunit = S.vunit;
       // a cut item is the CTA's first (place 0) or its last (place 1)
       const long long place = ((long long)blockIdx.x * 2 + (sg.blk0 > 0 ? 0 : 1)) * NT;
       if (tok < SUB) {
@@ -1196,24 +1222,34 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
         if (S.last) {
           __threadfence();
           const long long p0 = ((long long)c0 * 2 + (tree_unit(U, W, c0) > a0 ? 0 : 1)) * NT;  // (its first part)
+          // a warp per column, four channels a lane
 #pragma unroll 1
-          for (int j = h * SUB; j < h * SUB + SUB; ++j) {
+          for (int j = warp - 8; j < NT; j += 8) {
             const int row = S.row[j];
             if (row < 0) continue;
-            float m = -INFINITY, sum = 0.f, acc = 0.f;
+            float m = -INFINITY, sum = 0.f;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
             for (unsigned cc = c0; cc <= c1; ++cc) {
-              const long long sl = (cc == c0 ? p0 : (long long)cc * 2 * NT) + j;
-              const float mi = __ldcg(p.ws_ml + sl * 2), li = __ldcg(p.ws_ml + sl * 2 + 1);
-              const float oi = __ldcg(p.ws_o + sl * L.d + tok);
-              if (mi == -INFINITY) continue;
-              const float mn = fmaxf(m, mi);
-              const float fa = m == -INFINITY ? 0.f : exp2_approx(m - mn), fb = exp2_approx(mi - mn);
-              sum = sum * fa + li * fb;
-              acc = acc * fa + oi * fb;
+              const long long at = (cc == c0 ? p0 : (long long)cc * 2 * NT) + j;
+              const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.ws_ml) + at);
+              const float4 o = __ldcg(reinterpret_cast<const float4*>(p.ws_o + at * L.d) + lane);
+              if (ml.x == -INFINITY) continue;
+              const float mn = fmaxf(m, ml.x);
+              const float fa = m == -INFINITY ? 0.f : exp2_approx(m - mn), fb = exp2_approx(ml.x - mn);
+              sum = sum * fa + ml.y * fb;
+              acc.x = acc.x * fa + o.x * fb;
+              acc.y = acc.y * fa + o.y * fb;
+              acc.z = acc.z * fa + o.z * fb;
+              acc.w = acc.w * fa + o.w * fb;
               m = mn;
             }
-            put_out(p, row, tok, sum == 0.f ? 0.f : acc * (vunit / sum));
-            if (p.lse && tok == 0)
+            const float inv = sum == 0.f ? 0.f : vunit / sum;
+            put_out(p, row, 4 * lane, inv == 0.f ? 0.f : acc.x * inv);
+            put_out(p, row, 4 * lane + 1, inv == 0.f ? 0.f : acc.y * inv);
+            put_out(p, row, 4 * lane + 2, inv == 0.f ? 0.f : acc.z * inv);
+            put_out(p, row, 4 * lane + 3, inv == 0.f ? 0.f : acc.w * inv);
+            if (p.lse && lane == 0)
               p.lse[row] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.69314718055994531f;
           }
         }
