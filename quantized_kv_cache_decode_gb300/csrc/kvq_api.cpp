@@ -780,6 +780,7 @@ kvq_status tree_geometry(const LayerDesc& L, int batch, int columns, TreeGeom* G
   // the kernel counts the launch's blocks of 128 tokens in 32 bits
   const long long most = (max_seq_tokens(L) + kMaxNodes) / 128 + 2;
   if (most * batch > 0x7FFFFFFFLL / ((long long)L.H * G->chunks)) return KVQ_ERR_UNSUPPORTED;
+  if ((max_seq_tokens(L) / 16 + 8) * std::max(L.tpg, 1) >= (1LL << 32)) return KVQ_ERR_UNSUPPORTED;  // (see tile_record)
   // a quantized slot: 64 tokens, the headers of the records that they touch first
   int headers = 0;
   if (!L.fp8 && !L.bf16) headers = L.tpg == 1 ? 4 : (L.tpg % 4 == 0 ? 1 : 2);
@@ -861,6 +862,7 @@ kvq_status kvq_decode_attention_tree(const kvq_layer_config* cfg, const kvq_laye
   p.slot_bytes = G.slot_bytes;
   p.slot_hdr = G.slot_hdr;
   p.bf_tokens = G.bf_tokens;
+  p.tpg_inv = L.tpg > 1 ? (unsigned)(((1ull << 32) + L.tpg - 1) / L.tpg) : 0u;
   p.scale_log2 = softmax_scale * 1.4426950408889634f;
   p.ws_o = reinterpret_cast<float*>(ws);
   p.ws_ml = reinterpret_cast<float*>(ws + G.off_ml);

@@ -120,6 +120,7 @@ struct TreeParams {
   int nslots, slot_bytes;
   int slot_hdr;    // bytes of record headers at the start of a quantized slot
   int bf_tokens;   // bf16 tokens per slot (K rows, then V rows)
+  unsigned tpg_inv;  // ceil(2^32 / tiles per record), 0 where that is one tile
   float scale_log2;
   float* ws_o;     // [2 per CTA][NT][d] unnormalised partial outputs
   float* ws_ml;    // [2 per CTA][NT][2] maximum (log2 domain) and sum

@@ -202,7 +202,8 @@ struct TreeSmem {  // small shared state, after the big buffers
   uint32_t tmem;
   int abort;
   int last;                       // merge: this CTA finished the item
-  alignas(16) float m[128];       // running maximum of each column (log2 domain; 0 until one is set)
+  alignas(16) float neg[128];     // minus the running maximum of each column (log2 domain; 0 until one is set)
+  alignas(16) float rise[128];    // change of the maxima
   alignas(16) float fall[128];    // what a change of the maxima scales sums by; epilogue: 1 / sum
   alignas(16) float red[4][128];  // the four warps' maxima or sums
   int row[128];                   // epilogue: the columns' rows of the output, -1: none
@@ -235,6 +236,12 @@ __device__ __forceinline__ void tree_cursor(const TreeParams& p, const int* pre,
     else z = m - 1;
   }
   c.b = a;
+}
+
+// Record of tile t (t / tiles per record): t < 2^32 / tpg by the host's check, so that the
+// rounded-up reciprocal's excess (below tpg / 2^32 of t) does not reach the next integer
+__device__ __forceinline__ int tile_record(const TreeParams& p, int t) {
+  return p.tpg_inv ? (int)__umulhi((unsigned)t, p.tpg_inv) : t;
 }
 
 // First unit of CTA c of W
@@ -544,7 +551,7 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
               const uint8_t* rec = nullptr;
               int run = 0, within = 0;
               if (lane < 4 && t < ntile) {
-                const int r = t / L.tpg;
+                const int r = tile_record(p, t);
                 within = t - r * L.tpg;
                 if (lane == 0 || within == 0) {
                   rec = record_addr(L, p.C, sg.b, sg.h, r, p.status);
@@ -566,7 +573,7 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
               }
               __syncwarp();
               if (rec) {
-                if (hbytes) bulk_copy_g2s(smem_addr(dst + (t / L.tpg - t0 / L.tpg) * 1024), rec, hbytes, bar);
+                if (hbytes) bulk_copy_g2s(smem_addr(dst + (tile_record(p, t) - tile_record(p, t0)) * 1024), rec, hbytes, bar);
                 bulk_copy_g2s(smem_addr(dst + p.slot_hdr + lane * L.tile_bytes),
                               rec + L.hdr_bytes + (long long)within * L.tile_bytes, bytes, bar);
               }
@@ -691,8 +698,8 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
               if (quant) {
                 const uint32_t okmask = S.slot_ok[slot];
                 uint8_t* const src = slots + (size_t)slot * p.slot_bytes;
-                const int t0 = blk * 8 + i * 4, r0 = t0 / L.tpg;
-                const int last = 31 - __clz(okmask | 1u), nh = (t0 + last) / L.tpg - r0 + 1;
+                const int t0 = blk * 8 + i * 4, r0 = tile_record(p, t0);
+                const int last = 31 - __clz(okmask | 1u), nh = tile_record(p, t0 + last) - r0 + 1;
                 for (int e = 0; e < nh; ++e) {  // (a header whose tiles were not copied holds anything, and is not used)
                   const float4 sc = reinterpret_cast<const float4*>(src + e * 1024)[lane];
                   const float4 z = reinterpret_cast<const float4*>(src + e * 1024 + 512)[lane];
@@ -758,8 +765,13 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
     int slot = 0;
     uint32_t ph = 0, g = 0;
     bool ok = true, bad = false;
+    // byte offsets of the warp's first operand word and of its channels' scales in a tile (V)
+    const int lgv = F::kFp8 ? 7 : 31 - __clz(L.Gv);
+    const int vcode = 16 * F::kRb + (F::kBits == 8 ? (wq * 32 + lane) * 16
+                                                   : F::kBits == 4 ? ((wq >> 1) * 32 + lane) * 16 + (wq & 1) * 8 : lane * 16 + wq * 4);
+    const int vs0 = 32 * F::kRb + ((32 * wq) >> lgv) * 64 + q * 16, vs1 = 32 * F::kRb + ((32 * wq + 16) >> lgv) * 64 + q * 16;
     while (ok && tree_next(p, pre, lens, cur, sg)) {
-      const int blk1 = sg.blk1, nq = sg.nq;
+      const int blk1 = sg.blk1, nq = sg.nq, qn = sg.qn;
 #pragma unroll 1
       for (int blk = sg.blk0; ok && blk < blk1; ++blk, ++g) {
         const int buf = Sh::kKv == 2 ? (int)(g & 1) : 0;
@@ -780,7 +792,7 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
                 for (int e = 0; e < 2; ++e) {
                   const int ti = 2 * (wq & 1) + e;  // tile of the slot
                   if (!((okmask >> ti) & 1u)) continue;
-                  const uint8_t* const hdr = F::kFp8 ? src : src + ((t0 + ti) / L.tpg - t0 / L.tpg) * 1024;
+                  const uint8_t* const hdr = F::kFp8 ? src : src + (tile_record(p, t0 + ti) - tile_record(p, t0)) * 1024;
                   uint32_t w[F::kWords];
                   load_words<FMT>(src + p.slot_hdr + ti * L.tile_bytes, lane, w);
 #pragma unroll
@@ -792,41 +804,34 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
                 }
               }
             } else {
-              const int g0 = F::kFp8 ? 0 : 32 * wq / L.Gv, g1 = F::kFp8 ? 0 : (32 * wq + 16) / L.Gv;
-#pragma unroll 1
-              for (int tp = 0; tp < 4; tp += 2) {  // two tiles, channels 32 wq .. and 32 wq + 16 ..
+              const uint8_t* tile = src + p.slot_hdr;
+              // two tiles at a time, channels 32 wq .. and 32 wq + 16 ..
+              auto two = [&](int tp, uint32_t have) {
                 uint32_t f[2][8];
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                  const int ti = tp + u;
-                  // not in the store (behind the last tile, or a bad block): P is 0 there, so V must be finite
-#pragma unroll
-                  for (int e = 0; e < 2; ++e) f[e][4 * u] = f[e][4 * u + 1] = f[e][4 * u + 2] = f[e][4 * u + 3] = 0u;
-                  if ((okmask >> ti) & 1u) {
-                    const uint8_t* const tile = src + p.slot_hdr + ti * L.tile_bytes;
-                    const uint8_t* const codes = tile + 16 * F::kRb;
+                for (int u = 0; u < 2; ++u, tile += L.tile_bytes) {
+                  if (have >> u & 1u) {
                     uint32_t w[4];  // the words of steps 2 wq and 2 wq + 1
                     if constexpr (F::kBits == 8) {
-                      const uint4 v = *reinterpret_cast<const uint4*>(codes + (wq * 32 + lane) * 16);
+                      const uint4 v = *reinterpret_cast<const uint4*>(tile + vcode);
                       w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
                     } else if constexpr (F::kBits == 4) {
-                      const uint2 v =
-                          *reinterpret_cast<const uint2*>(codes + ((wq >> 1) * 32 + lane) * 16 + (wq & 1) * 8);
+                      const uint2 v = *reinterpret_cast<const uint2*>(tile + vcode);
                       w[0] = v.x, w[1] = v.y;
                     } else {
-                      w[0] = *reinterpret_cast<const uint32_t*>(codes + lane * 16 + wq * 4);
+                      w[0] = *reinterpret_cast<const uint32_t*>(tile + vcode);
                       w[1] = w[0] >> 8;
                     }
                     uint4 s0 = make_uint4(0, 0, 0, 0), s1 = s0;  // scales of the two steps' channels
                     if constexpr (!F::kFp8) {
-                      s0 = *reinterpret_cast<const uint4*>(tile + 32 * F::kRb + g0 * 64 + q * 16);
-                      s1 = *reinterpret_cast<const uint4*>(tile + 32 * F::kRb + g1 * 64 + q * 16);
+                      s0 = *reinterpret_cast<const uint4*>(tile + vs0);
+                      s1 = *reinterpret_cast<const uint4*>(tile + vs1);
                     }
                     v_frag<FMT>(w, 0, s0, f[0] + 4 * u);
                     v_frag<FMT>(w + (F::kBits == 8 ? 2 : 1), 0, s1, f[1] + 4 * u);
                     if constexpr (F::kFp8) {
                       // tokens behind the last one of a partly filled tile: zeros whatever the store holds
-                      const int nv = sg.qn - 16 * (t0 + ti);
+                      const int nv = qn - 16 * (t0 + tp + u);
                       if (nv < 16) {
                         const uint32_t m0 = pair_mask(2 * q, nv), m1 = pair_mask(2 * q + 8, nv);
 #pragma unroll
@@ -836,11 +841,22 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
                         }
                       }
                     }
+                  } else {
+                    // not in the store (behind the last tile, or a bad block): P is 0 there, so V must be finite
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) f[e][4 * u] = f[e][4 * u + 1] = f[e][4 * u + 2] = f[e][4 * u + 3] = 0u;
                   }
                 }
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
                   tc_st_frag2(tt + ((uint32_t)(16 * e) << 16) + 32 * half + 8 * tp, f[e]);
+              };
+              if (okmask == 15u) {
+                two(0, 3u);
+                two(2, 3u);
+              } else {
+#pragma unroll 1
+                for (int tp = 0; tp < 4; tp += 2) two(tp, okmask >> tp);
               }
             }
             __syncwarp();
@@ -931,13 +947,13 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
     const int tok = 32 * wq + lane;       // the thread's tensor-memory lane: token of the scores, channel of the outputs
     const int th = tid - 256;             // 0 .. 255 over both halves
     const uint32_t tlane = tm + ((uint32_t)(32 * wq) << 16);
-    float* const ms = S.m + h * SUB;
+    float* const neg = S.neg + h * SUB;
     const int barid = 1 + h;
     uint32_t g = 0;
     while (tree_next(p, pre, lens, cur, sg)) {
       // ---- the drafted tokens, where this cut reaches a block of theirs ----
-      named_sync(3, 256);  // (the previous cut's epilogue has read S.m)
-      if (th < NT) S.m[th] = 0.f;
+      named_sync(3, 256);  // (the previous cut's epilogue has read S.neg)
+      if (th < NT) S.neg[th] = 0.f;
       if (th < 64 && sg.blk1 > sg.nq + (sg.n_sink + sg.r) / kBlk) {
         bool wild = false;
         if (th < p.N) {
@@ -995,7 +1011,7 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
       if (th < p.N && sg.blk1 > sg.nq + (sg.n_sink + sg.r) / kBlk) S.anc[th] = tree_ancestors(S.par, th);
       named_sync(3, 256);
 
-      constexpr int kCh = SUB == 64 ? 16 : SUB;  // columns in registers at a time
+      constexpr int kCh = 16;  // columns in registers at a time
       float l[SUB];
 #pragma unroll
       for (int j = 0; j < SUB; ++j) l[j] = 0.f;
@@ -1039,18 +1055,16 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
         }
         const float c = F::kFp8 && quant ? p.scale_log2 * S.kscale : p.scale_log2;
         tree_wait(&S.s_full[sb], (g >> 1) & 1, abort, p.status);
+        if (g > 1) tree_wait(&S.p_free[sb], ((g >> 1) - 1) & 1, abort, p.status);  // P's buffer has been read
         tc_fence_after();
-        // columns c0 .. of the scores: exponents (log2) relative to the columns' maxima so far
-        float x[kCh];
-        auto scores = [&](int c0) {
-#pragma unroll
-          for (int j = 0; j < kCh; j += 16) tc_ld16(ts + c0 + j, x + j);
-          tc_wait_ld();
+        // Columns c0 .. of the scores as exponents (log2) relative to the columns' maxima so far, and their largest
+        auto exponents = [&](int c0, float (&x)[kCh], float& top) {
+          float t0 = -INFINITY, t1 = -INFINITY;
 #pragma unroll
           for (int j = 0; j < kCh; j += 4) {
-            const float4 m4 = *reinterpret_cast<const float4*>(ms + c0 + j);
-            const float2 a = fma_f32x2(make_float2(x[j], x[j + 1]), make_float2(c, c), make_float2(-m4.x, -m4.y));
-            const float2 b = fma_f32x2(make_float2(x[j + 2], x[j + 3]), make_float2(c, c), make_float2(-m4.z, -m4.w));
+            const float4 m4 = *reinterpret_cast<const float4*>(neg + c0 + j);
+            const float2 a = fma_f32x2(make_float2(x[j], x[j + 1]), make_float2(c, c), make_float2(m4.x, m4.y));
+            const float2 b = fma_f32x2(make_float2(x[j + 2], x[j + 3]), make_float2(c, c), make_float2(m4.z, m4.w));
             x[j] = a.x;
             x[j + 1] = a.y;
             x[j + 2] = b.x;
@@ -1061,22 +1075,56 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
 #pragma unroll
             for (int j = 0; j < kCh; ++j) x[j] = (w >> j) & 1u ? (spoilt ? NAN : x[j]) : -INFINITY;
           }
+#pragma unroll
+          for (int j = 0; j < kCh; j += 4) {
+            t0 = fmaxf(fmaxf(x[j], x[j + 1]), t0);
+            t1 = fmaxf(fmaxf(x[j + 2], x[j + 3]), t1);
+          }
+          top = fmaxf(top, fmaxf(t0, t1));
         };
+        uint8_t* const P = Ps + sb * Sh::kPBytes + (NT == 128 ? h * (kBlk * 128) : 0);
+        auto put_p = [&](int col, const float* e) {  // eight columns
+          const uint32_t at = (uint32_t)(tok * Sh::kPRow + (NT == 128 ? 0 : h * SUB * 2) + col * 2);
+          *reinterpret_cast<uint4*>(P + (at ^ (((at >> 7) & Sh::kPMask) << 4))) =
+              make_uint4(pack_f16(e[0], e[1]), pack_f16(e[2], e[3]), pack_f16(e[4], e[5]), pack_f16(e[6], e[7]));
+        };
+        // One pass: P and the sums with the maxima as they are; whether one rose too far shows at the end.
+        // (an exponent above kCap, whose power the sums could not hold, is cut to it: that column is done over)
+        constexpr float kCap = 100.f;
         float top = -INFINITY;
+        float xa[kCh], xb[kCh];
+        tc_ld16(ts, xa);
 #pragma unroll
         for (int c0 = 0; c0 < SUB; c0 += kCh) {
-          scores(c0);
+          float(&x)[kCh] = (c0 / kCh) & 1 ? xb : xa;
+          tc_wait_ld();
+          if (c0 + kCh < SUB) tc_ld16(ts + c0 + kCh, (c0 / kCh) & 1 ? xa : xb);
+          exponents(c0, x, top);
+          if (__any_sync(kAll, top > kCap)) {
 #pragma unroll
-          for (int j = 0; j < kCh; j += 2) top = fmaxf(fmaxf(x[j], x[j + 1]), top);
+            for (int j = 0; j < kCh; ++j) x[j] = fminf(x[j], kCap);
+          }
+#pragma unroll
+          for (int j = 0; j < kCh; j += 2) {
+            x[j] = exp2_approx(x[j]);
+            x[j + 1] = exp2_approx(x[j + 1]);
+            const float2 n = add_f32x2(make_float2(l[c0 + j], l[c0 + j + 1]), make_float2(x[j], x[j + 1]));
+            l[c0 + j] = n.x;
+            l[c0 + j + 1] = n.y;
+          }
+          put_p(c0, x);
+          put_p(c0 + 8, x + 8);
         }
         if (named_any(barid, 128, unset || !(top <= 8.f))) {
-          // ---- new column maxima over the block's 128 tokens ----
+          // ---- a maximum is new or rose by more than 8: the block's column maxima ----
 #pragma unroll 1
           for (int c0 = 0; c0 < SUB; c0 += kCh) {
-            scores(c0);
+            tc_ld16(ts + c0, xa);
+            tc_wait_ld();
+            exponents(c0, xa, top);
 #pragma unroll
             for (int j = 0; j < kCh; ++j) {
-              float v = x[j];
+              float v = xa[j];
 #pragma unroll
               for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
               if (lane == 0) S.red[wq][h * SUB + c0 + j] = v;
@@ -1092,19 +1140,28 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
               has = d != -INFINITY;
               rise = has ? d : 0.f;
             }
-            S.m[j] += rise;
+            S.rise[j] = rise;
             S.fall[j] = exp2_approx(-rise);
             if (!has) S.unset[h] = 1;
           }
           named_sync(barid, 128);
           unset = S.unset[h] != 0;
+          // the sums and P over: this block's share l took in is taken out again (its rounding is scaled
+          // down with the sum: at most 2^-24 of the new one), the rest scaled, the new share put in
 #pragma unroll
-          for (int j = 0; j < SUB; j += 4) {
-            const float4 f = *reinterpret_cast<const float4*>(&S.fall[h * SUB + j]);
-            l[j] = scaled(l[j], f.x);
-            l[j + 1] = scaled(l[j + 1], f.y);
-            l[j + 2] = scaled(l[j + 2], f.z);
-            l[j + 3] = scaled(l[j + 3], f.w);
+          for (int c0 = 0; c0 < SUB; c0 += kCh) {
+            tc_ld16(ts + c0, xa);
+            tc_wait_ld();
+            exponents(c0, xa, top);
+#pragma unroll
+            for (int j = 0; j < kCh; ++j) {
+              const float d = S.rise[h * SUB + c0 + j], f = S.fall[h * SUB + c0 + j];
+              const float rest = l[c0 + j] - exp2_approx(fminf(xa[j], kCap));
+              xa[j] = exp2_approx(xa[j] - d);
+              l[c0 + j] = scaled(rest, f) + xa[j];
+            }
+            put_p(c0, xa);
+            put_p(c0 + 8, xa + 8);
           }
           if (blk > blk0) {  // what O holds so far, behind the previous block's product
             tree_wait(&S.p_free[(g - 1) & 1], ((g - 1) >> 1) & 1, abort, p.status);
@@ -1120,40 +1177,18 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
             }
             tc_wait_st();
           }
-          named_sync(barid, 128);  // (fall and unset have been read)
+          named_sync(barid, 128);  // (neg, rise, fall and unset have been read)
+          if (tok < SUB) neg[tok] -= S.rise[h * SUB + tok];
           if (tok == 0) S.unset[h] = 0;
-          if (kCh == SUB) scores(0);
-        }
-        // ---- P, where the product that read its buffer last is done ----
-        if (g > 1) tree_wait(&S.p_free[sb], ((g >> 1) - 1) & 1, abort, p.status);
-        uint8_t* const P = Ps + sb * Sh::kPBytes + (NT == 128 ? h * (kBlk * 128) : 0);
-#pragma unroll
-        for (int c0 = 0; c0 < SUB; c0 += kCh) {
-          if (kCh < SUB) scores(c0);
-          if (c0 + kCh == SUB) {  // the last read of S
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_addr(&S.s_free[sb]));
-          }
-#pragma unroll
-          for (int j = 0; j < kCh; j += 8) {
-            uint32_t w[4];
-#pragma unroll
-            for (int i = 0; i < 8; i += 2) {
-              const float2 e = make_float2(exp2_approx(x[j + i]), exp2_approx(x[j + i + 1]));
-              const float2 n = add_f32x2(make_float2(l[c0 + j + i], l[c0 + j + i + 1]), e);
-              l[c0 + j + i] = n.x;
-              l[c0 + j + i + 1] = n.y;
-              w[i >> 1] = pack_f16(e.x, e.y);
-            }
-            const uint32_t at = (uint32_t)(tok * Sh::kPRow + (NT == 128 ? 0 : h * SUB * 2) + (c0 + j) * 2);
-            *reinterpret_cast<uint4*>(P + (at ^ (((at >> 7) & Sh::kPMask) << 4))) = make_uint4(w[0], w[1], w[2], w[3]);
-          }
+          named_sync(barid, 128);
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&S.p_full[sb]));
+        if (lane == 0) {
+          mbar_arrive(smem_addr(&S.s_free[sb]));
+          mbar_arrive(smem_addr(&S.p_full[sb]));
+        }
       }
 
       // ---- epilogue: column sums, then O ----
@@ -1179,10 +1214,10 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
           const int n = col / p.gh;
           row = (sg.b * p.N + n) * p.Hq + sg.h * p.gh + (col - n * p.gh);
           if (!whole) {
-            p.ws_ml[(place + j) * 2] = sum == 0.f ? -INFINITY : S.m[j];
+            p.ws_ml[(place + j) * 2] = sum == 0.f ? -INFINITY : -S.neg[j];
             p.ws_ml[(place + j) * 2 + 1] = sum;
           } else if (p.lse) {
-            p.lse[row] = sum == 0.f ? -INFINITY : (S.m[j] + log2f(sum)) * 0.69314718055994531f;
+            p.lse[row] = sum == 0.f ? -INFINITY : (log2f(sum) - S.neg[j]) * 0.69314718055994531f;
           }
         }
         S.row[j] = row;
