@@ -130,6 +130,11 @@ __device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) {
   asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
+__device__ __forceinline__ float warp_max(float v) {  // (NaN only where all are)
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
 // one lane of the warp
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
@@ -168,9 +173,11 @@ struct TreeShape {
   static constexpr int kQBytes = NT * 256;         // queries (f16): [two 64-channel halves][NT rows of 128 bytes]
   static constexpr int kPBytes = kBlk * NT * 2;    // one buffer of P (f16)
   static constexpr int kFixed = kQBytes + 2 * kPBytes;
-  // tensor memory: scores and outputs take NT columns each (scores twice), K and V 64 each, twice where there is room
-  static constexpr int kKv = NT == 128 ? 1 : 2;
-  static constexpr uint32_t kTmK = 0, kTmV = 64 * kKv, kTmS = 128 * kKv, kTmO = 128 * kKv + 2 * NT;
+  // tensor memory: K and V twice 64 columns each, outputs NT, scores NT, twice where there is room (with 128
+  // columns one buffer of scores and two of K and V measured faster than the other way round, 8192-token INT4
+  // items of 128 columns: see the note on the roles' latencies above the kernel)
+  static constexpr int kSb = NT == 128 ? 1 : 2;
+  static constexpr uint32_t kTmK = 0, kTmV = 128, kTmS = 256, kTmO = 256 + kSb * NT;
   static_assert(kTmO + NT <= 512, "tensor memory");
   // P rows (one per token): NT <= 64 columns in one row of 2 NT bytes, 128 as two 64-column regions, in the
   // swizzle of that row length (B operand with the columns contiguous)
@@ -203,7 +210,6 @@ struct TreeSmem {  // small shared state, after the big buffers
   int abort;
   int last;                       // merge: this CTA finished the item
   alignas(16) float neg[128];     // minus the running maximum of each column (log2 domain; 0 until one is set)
-  alignas(16) float rise[128];    // change of the maxima
   alignas(16) float fall[128];    // what a change of the maxima scales sums by; epilogue: 1 / sum
   alignas(16) float red[4][128];  // the four warps' maxima or sums
   int row[128];                   // epilogue: the columns' rows of the output, -1: none
@@ -638,9 +644,9 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
 #pragma unroll 1
         for (int i = 0; ok && i <= nb; ++i) {
           if (i < nb) {
-            const uint32_t kb = Sh::kKv == 2 ? g & 1 : 0, kph = Sh::kKv == 2 ? (g >> 1) & 1 : g & 1, sb = g & 1;
+            const uint32_t kb = g & 1, kph = (g >> 1) & 1, sb = Sh::kSb == 2 ? g & 1 : 0;
             ok = tree_wait(&S.k_full[kb], kph, abort, p.status);
-            if (ok && g > 1) ok = tree_wait(&S.s_free[sb], ((g >> 1) - 1) & 1, abort, p.status);
+            if (ok && g >= Sh::kSb) ok = tree_wait(&S.s_free[sb], ((g / Sh::kSb) - 1) & 1, abort, p.status);
             if (!__all_sync(kAll, ok)) { ok = false; break; }
             tc_fence_after();
             if (elect_one()) {
@@ -654,10 +660,9 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
             __syncwarp();
           }
           if (i > 0) {
-            const uint32_t pg = g - 1, vb = Sh::kKv == 2 ? pg & 1 : 0, vph = Sh::kKv == 2 ? (pg >> 1) & 1 : pg & 1,
-                           pb = pg & 1;
-            ok = tree_wait(&S.v_full[vb], vph, abort, p.status);
-            if (ok) ok = tree_wait(&S.p_full[pb], (pg >> 1) & 1, abort, p.status);
+            const uint32_t pg = g - 1, vb = pg & 1, pb = vb, ph = (pg >> 1) & 1;
+            ok = tree_wait(&S.v_full[vb], ph, abort, p.status);
+            if (ok) ok = tree_wait(&S.p_full[pb], ph, abort, p.status);
             if (!__all_sync(kAll, ok)) { ok = false; break; }
             tc_fence_after();
             if (elect_one()) {
@@ -774,9 +779,9 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
       const int blk1 = sg.blk1, nq = sg.nq, qn = sg.qn;
 #pragma unroll 1
       for (int blk = sg.blk0; ok && blk < blk1; ++blk, ++g) {
-        const int buf = Sh::kKv == 2 ? (int)(g & 1) : 0;
+        const int buf = (int)(g & 1);
         // the buffer's previous use has been read
-        if (!(ok = tree_wait(&empty[buf], (Sh::kKv == 2 ? (g >> 1) & 1 : g & 1) ^ 1, abort, p.status))) break;
+        if (!(ok = tree_wait(&empty[buf], ((g >> 1) & 1) ^ 1, abort, p.status))) break;
         tc_fence_after();
         const uint32_t tt = tlane + buf * 64;
         if (blk < nq) {
@@ -1018,16 +1023,17 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
       bool unset = true;  // some column has no maximum yet (uniform over the warpgroup)
       bool has = false;   // column `tok` has one
 
-      const int blk0 = sg.blk0, blk1 = sg.blk1;
+      const int blk0 = sg.blk0, blk1 = sg.blk1, nq = sg.nq;
+      const int nplain = L.paged ? 0 : sg.qn / kBlk;  // leading blocks whose tokens all count
 #pragma unroll 1
       for (int blk = blk0; blk < blk1; ++blk, ++g) {
-        const uint32_t sb = g & 1;
+        const uint32_t sb = Sh::kSb == 2 ? g & 1 : 0, pb = g & 1;
         const uint32_t ts = tlane + Sh::kTmS + sb * NT + h * SUB, to = tlane + Sh::kTmO + h * SUB;
         // ---- which of the half's columns see the thread's token ----
-        const bool quant = blk < sg.nq;
+        const bool quant = blk < nq;
         bool masked = false, spoilt = false;
         unsigned long long allow = ~0ull;
-        if (!quant || L.paged || blk * kBlk + kBlk > sg.qn) {
+        if (blk >= nplain) {
           bool valid;
           if (quant) {
             const int x = blk * kBlk + tok;
@@ -1038,7 +1044,7 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
             }
             allow = valid ? ~0ull : 0ull;
           } else {
-            const int nsr = sg.n_sink + sg.r, x = (blk - sg.nq) * kBlk + tok;
+            const int nsr = sg.n_sink + sg.r, x = (blk - nq) * kBlk + tok;
             valid = x < nsr;
             if (!valid) allow = 0;
             if (x >= nsr && x < nsr + p.N) {  // a drafted token: its descendants' columns
@@ -1054,8 +1060,8 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
           masked = __any_sync(kAll, !valid);
         }
         const float c = F::kFp8 && quant ? p.scale_log2 * S.kscale : p.scale_log2;
-        tree_wait(&S.s_full[sb], (g >> 1) & 1, abort, p.status);
-        if (g > 1) tree_wait(&S.p_free[sb], ((g >> 1) - 1) & 1, abort, p.status);  // P's buffer has been read
+        tree_wait(&S.s_full[sb], (g / Sh::kSb) & 1, abort, p.status);
+        if (g > 1) tree_wait(&S.p_free[pb], ((g >> 1) - 1) & 1, abort, p.status);  // P's buffer has been read
         tc_fence_after();
         // Columns c0 .. of the scores as exponents (log2) relative to the columns' maxima so far, and their largest
         auto exponents = [&](int c0, float (&x)[kCh], float& top) {
@@ -1082,122 +1088,141 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
           }
           top = fmaxf(top, fmaxf(t0, t1));
         };
-        uint8_t* const P = Ps + sb * Sh::kPBytes + (NT == 128 ? h * (kBlk * 128) : 0);
+        uint8_t* const P = Ps + pb * Sh::kPBytes + (NT == 128 ? h * (kBlk * 128) : 0);
         auto put_p = [&](int col, const float* e) {  // eight columns
           const uint32_t at = (uint32_t)(tok * Sh::kPRow + (NT == 128 ? 0 : h * SUB * 2) + col * 2);
           *reinterpret_cast<uint4*>(P + (at ^ (((at >> 7) & Sh::kPMask) << 4))) =
               make_uint4(pack_f16(e[0], e[1]), pack_f16(e[2], e[3]), pack_f16(e[4], e[5]), pack_f16(e[6], e[7]));
         };
-        // One pass: P and the sums with the maxima as they are; whether one rose too far shows at the end.
-        // (an exponent above kCap, whose power the sums could not hold, is cut to it: that column is done over)
-        constexpr float kCap = 100.f;
-        float top = -INFINITY;
+        // P and the sums in one pass, with the maxima as they are; whether one rose too far shows at its end.
+        // (a power beyond what the sums could give back is cut to kCap; its column is done over)
+        constexpr float kCap = 1.2676506e30f;  // 2^100
+        bool fresh = unset, again = false;     // the block's column maxima first; the pass for a second time
         float xa[kCh], xb[kCh];
-        tc_ld16(ts, xa);
-#pragma unroll
-        for (int c0 = 0; c0 < SUB; c0 += kCh) {
-          float(&x)[kCh] = (c0 / kCh) & 1 ? xb : xa;
-          tc_wait_ld();
-          if (c0 + kCh < SUB) tc_ld16(ts + c0 + kCh, (c0 / kCh) & 1 ? xa : xb);
-          exponents(c0, x, top);
-          if (__any_sync(kAll, top > kCap)) {
-#pragma unroll
-            for (int j = 0; j < kCh; ++j) x[j] = fminf(x[j], kCap);
-          }
-#pragma unroll
-          for (int j = 0; j < kCh; j += 2) {
-            x[j] = exp2_approx(x[j]);
-            x[j + 1] = exp2_approx(x[j + 1]);
-            const float2 n = add_f32x2(make_float2(l[c0 + j], l[c0 + j + 1]), make_float2(x[j], x[j + 1]));
-            l[c0 + j] = n.x;
-            l[c0 + j + 1] = n.y;
-          }
-          put_p(c0, x);
-          put_p(c0 + 8, x + 8);
-        }
-        if (named_any(barid, 128, unset || !(top <= 8.f))) {
-          // ---- a maximum is new or rose by more than 8: the block's column maxima ----
 #pragma unroll 1
-          for (int c0 = 0; c0 < SUB; c0 += kCh) {
-            tc_ld16(ts + c0, xa);
-            tc_wait_ld();
-            exponents(c0, xa, top);
-#pragma unroll
-            for (int j = 0; j < kCh; ++j) {
-              float v = xa[j];
-#pragma unroll
-              for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
-              if (lane == 0) S.red[wq][h * SUB + c0 + j] = v;
-            }
-          }
-          named_sync(barid, 128);
-          if (tok < SUB) {
-            const int j = h * SUB + tok;
-            // d: the block's maximum relative to the column's so far; its first one is taken as it is
-            const float d = fmaxf(fmaxf(S.red[0][j], S.red[1][j]), fmaxf(S.red[2][j], S.red[3][j]));
-            float rise = fmaxf(d, 0.f);
-            if (!has) {
-              has = d != -INFINITY;
-              rise = has ? d : 0.f;
-            }
-            S.rise[j] = rise;
-            S.fall[j] = exp2_approx(-rise);
-            if (!has) S.unset[h] = 1;
-          }
-          named_sync(barid, 128);
-          unset = S.unset[h] != 0;
-          // the sums and P over: this block's share l took in is taken out again (its rounding is scaled
-          // down with the sum: at most 2^-24 of the new one), the rest scaled, the new share put in
-#pragma unroll
-          for (int c0 = 0; c0 < SUB; c0 += kCh) {
-            tc_ld16(ts + c0, xa);
-            tc_wait_ld();
-            exponents(c0, xa, top);
-#pragma unroll
-            for (int j = 0; j < kCh; ++j) {
-              const float d = S.rise[h * SUB + c0 + j], f = S.fall[h * SUB + c0 + j];
-              const float rest = l[c0 + j] - exp2_approx(fminf(xa[j], kCap));
-              xa[j] = exp2_approx(xa[j] - d);
-              l[c0 + j] = scaled(rest, f) + xa[j];
-            }
-            put_p(c0, xa);
-            put_p(c0 + 8, xa + 8);
-          }
-          if (blk > blk0) {  // what O holds so far, behind the previous block's product
-            tree_wait(&S.p_free[(g - 1) & 1], ((g - 1) >> 1) & 1, abort, p.status);
-            tc_fence_after();
+        while (true) {
+          if (fresh) {
+            // ---- the block's column maxima ----
+            float top = -INFINITY;
 #pragma unroll 1
-            for (int j0 = 0; j0 < SUB; j0 += 8) {
-              float o[8];
-              tc_ld8(to + j0, o);
+            for (int c0 = 0; c0 < SUB; c0 += kCh) {
+              tc_ld16(ts + c0, xa);
               tc_wait_ld();
+              exponents(c0, xa, top);
+              float mine = 0.f;
 #pragma unroll
-              for (int j = 0; j < 8; ++j) o[j] = scaled(o[j], S.fall[h * SUB + j0 + j]);
-              tc_st8(to + j0, o);
+              for (int j = 0; j < kCh; ++j) {
+                const float v = warp_max(xa[j]);
+                if (lane == j) mine = v;
+              }
+              if (lane < kCh) S.red[wq][h * SUB + c0 + lane] = mine;
             }
-            tc_wait_st();
+            named_sync(barid, 128);
+            if (tok < SUB) {
+              const int j = h * SUB + tok;
+              // d: the block's maximum relative to the column's so far; its first one is taken as it is
+              const float d = fmaxf(fmaxf(S.red[0][j], S.red[1][j]), fmaxf(S.red[2][j], S.red[3][j]));
+              float rise = fmaxf(d, 0.f);
+              if (!has) {
+                has = d != -INFINITY;
+                rise = has ? d : 0.f;
+              }
+              neg[tok] -= rise;
+              S.fall[j] = exp2_approx(-rise);
+              if (!has) S.unset[h] = 1;
+            }
+            named_sync(barid, 128);
+            unset = S.unset[h] != 0;
+            if (blk > blk0) {  // what the sums and O hold so far (O: behind the previous block's product)
+#pragma unroll
+              for (int j = 0; j < SUB; j += 4) {
+                const float4 f = *reinterpret_cast<const float4*>(&S.fall[h * SUB + j]);
+                l[j] = scaled(l[j], f.x);
+                l[j + 1] = scaled(l[j + 1], f.y);
+                l[j + 2] = scaled(l[j + 2], f.z);
+                l[j + 3] = scaled(l[j + 3], f.w);
+              }
+              tree_wait(&S.p_free[(g - 1) & 1], ((g - 1) >> 1) & 1, abort, p.status);
+              tc_fence_after();
+#pragma unroll 1
+              for (int j0 = 0; j0 < SUB; j0 += 8) {
+                float o[8];
+                tc_ld8(to + j0, o);
+                tc_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 8; ++j) o[j] = scaled(o[j], S.fall[h * SUB + j0 + j]);
+                tc_st8(to + j0, o);
+              }
+              tc_wait_st();
+            }
+            named_sync(barid, 128);  // (fall and unset have been read)
+            if (tok == 0) S.unset[h] = 0;
           }
-          named_sync(barid, 128);  // (neg, rise, fall and unset have been read)
-          if (tok < SUB) neg[tok] -= S.rise[h * SUB + tok];
-          if (tok == 0) S.unset[h] = 0;
-          named_sync(barid, 128);
+          float top = -INFINITY;
+          tc_ld16(ts, xa);
+#pragma unroll
+          for (int c0 = 0; c0 < SUB; c0 += kCh) {
+            float(&x)[kCh] = (c0 / kCh) & 1 ? xb : xa;
+            tc_wait_ld();
+            if (c0 + kCh < SUB) tc_ld16(ts + c0 + kCh, (c0 / kCh) & 1 ? xa : xb);
+            exponents(c0, x, top);
+            const bool hot = __any_sync(kAll, top > 99.f);
+#pragma unroll
+            for (int j = 0; j < kCh; ++j) x[j] = exp2_approx(x[j]);
+            if (hot) {
+#pragma unroll
+              for (int j = 0; j < kCh; ++j) x[j] = fminf(x[j], kCap);
+            }
+#pragma unroll
+            for (int j = 0; j < kCh; j += 2) {
+              const float2 n = add_f32x2(make_float2(l[c0 + j], l[c0 + j + 1]), make_float2(x[j], x[j + 1]));
+              l[c0 + j] = n.x;
+              l[c0 + j + 1] = n.y;
+            }
+            put_p(c0, x);
+            put_p(c0 + 8, x + 8);
+          }
+          if (!named_any(barid, 128, top > 8.f) || again) break;
+          // ---- a maximum rose by more than 8: the block over, with new maxima.  Its share is taken out of the
+          // sums again (what that rounds is scaled down with them: at most 2^-24 of the new sum) ----
+#pragma unroll
+          for (int c0 = 0; c0 < SUB; c0 += kCh) {
+            tc_ld16(ts + c0, xa);
+            tc_wait_ld();
+            exponents(c0, xa, top);
+#pragma unroll
+            for (int j = 0; j < kCh; ++j) l[c0 + j] -= fminf(exp2_approx(xa[j]), kCap);
+          }
+          named_sync(barid, 128);  // (the old maxima have been read)
+          fresh = again = true;
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(smem_addr(&S.s_free[sb]));
-          mbar_arrive(smem_addr(&S.p_full[sb]));
+          mbar_arrive(smem_addr(&S.p_full[pb]));
         }
       }
 
       // ---- epilogue: column sums, then O ----
+      // a lane's sums of all columns -> all lanes' sum of 2 lane, 2 lane + 1 (32 columns: lane; 16: lane / 2):
+      // each step halves the columns a lane keeps and adds the partner's for those
 #pragma unroll
-      for (int j = 0; j < SUB; ++j) {
-        float v = l[j];
+      for (int w = SUB / 2, bit = 16; bit > 0; w >>= 1, bit >>= 1) {
+        const bool up = (lane & bit) != 0;
+        if (w == 0) l[0] += __shfl_xor_sync(kAll, l[0], bit);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
-        if (lane == 0) S.red[wq][h * SUB + j] = v;
+        for (int j = 0; j < w; ++j) {
+          const float keep = up ? l[j + w] : l[j], give = up ? l[j] : l[j + w];
+          l[j] = keep + __shfl_xor_sync(kAll, give, bit);
+        }
+      }
+      if constexpr (SUB == 64) {
+        S.red[wq][h * SUB + 2 * lane] = l[0];
+        S.red[wq][h * SUB + 2 * lane + 1] = l[1];
+      } else if (SUB == 32 || (lane & 1) == 0) {
+        S.red[wq][h * SUB + (SUB == 32 ? lane : lane >> 1)] = l[0];
       }
       tree_wait(&S.p_free[(g - 1) & 1], ((g - 1) >> 1) & 1, abort, p.status);
       tc_fence_after();
