@@ -781,11 +781,11 @@ kvq_status tree_geometry(const LayerDesc& L, int batch, int columns, TreeGeom* G
   const long long most = (max_seq_tokens(L) + kMaxNodes) / 128 + 2;
   if (most * batch > 0x7FFFFFFFLL / ((long long)L.H * G->chunks)) return KVQ_ERR_UNSUPPORTED;
   if ((max_seq_tokens(L) / 16 + 8) * std::max(L.tpg, 1) >= (1LL << 32)) return KVQ_ERR_UNSUPPORTED;  // (see tile_record)
-  // a quantized slot: 64 tokens, the headers of the records that they touch first
-  int headers = 0;
-  if (!L.fp8 && !L.bf16) headers = L.tpg == 1 ? 4 : (L.tpg % 4 == 0 ? 1 : 2);
-  G->slot_hdr = headers * 1024;
-  const int need = L.bf16 ? 0 : G->slot_hdr + 4 * L.tile_bytes;
+  // a quantized slot: the bytes of 8 tiles with the headers of the records that begin there, behind room
+  // for the header of a record that began earlier
+  const int headers = L.fp8 || L.bf16 ? 0 : (8 + L.tpg - 1) / L.tpg;
+  G->slot_hdr = headers ? L.hdr_bytes : 0;
+  const int need = L.bf16 ? 0 : G->slot_hdr + 8 * L.tile_bytes + headers * L.hdr_bytes;
   G->slot_bytes = (std::max(need, L.bf16 ? 32768 : 16384) + 127) / 128 * 128;
   G->bf_tokens = G->slot_bytes >= 32768 ? 64 : 32;
   const size_t fixed = tree_fixed_smem(G->nt, batch);

@@ -118,7 +118,7 @@ struct TreeParams {
   int N, Hq, gh, batch;
   int chunks;      // column chunks of NT per (sequence, kv head)
   int nslots, slot_bytes;
-  int slot_hdr;    // bytes of record headers at the start of a quantized slot
+  int slot_hdr;    // bytes of a quantized slot before the block's own (integer layers: a record header)
   int bf_tokens;   // bf16 tokens per slot (K rows, then V rows)
   unsigned tpg_inv;  // ceil(2^32 / tiles per record), 0 where that is one tile
   float scale_log2;

@@ -250,6 +250,26 @@ __device__ __forceinline__ int tile_record(const TreeParams& p, int t) {
   return p.tpg_inv ? (int)__umulhi((unsigned)t, p.tpg_inv) : t;
 }
 
+// A quantized slot holds one block's bytes as they lie in memory, behind kPreHdr bytes (integer layers) for the
+// header of a record that began in an earlier block: [header] tile tile .. [header] tile ..
+struct TileMap {
+  int t0, r0, own;  // first tile, its record, whether that record begins here
+  __device__ __forceinline__ TileMap(const TreeParams& p, int blk) {
+    t0 = blk * 8;
+    r0 = tile_record(p, t0);
+    own = r0 * p.L.tpg == t0;
+  }
+  // bytes to tile j (0 .. 7) of the block, given its record's number behind r0
+  __device__ __forceinline__ int tile(const TreeParams& p, int j, int e) const {
+    return p.slot_hdr + j * p.L.tile_bytes + (e + own) * p.L.hdr_bytes;
+  }
+  // bytes to the header of record r0 + e
+  __device__ __forceinline__ int header(const TreeParams& p, int e) const {
+    return e + own == 0 ? 0 : tile(p, e == 0 ? 0 : (r0 + e) * p.L.tpg - t0, e) - p.L.hdr_bytes;
+  }
+  __device__ __forceinline__ int record(const TreeParams& p, int j) const { return tile_record(p, t0 + j) - r0; }
+};
+
 // First unit of CTA c of W
 __device__ __forceinline__ unsigned tree_unit(unsigned U, unsigned W, unsigned c) {
   return (unsigned)((unsigned long long)U * c / W);
@@ -546,47 +566,41 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
         const int blk1 = sg.blk1, nq = sg.nq, qn = sg.qn;
         for (int blk = sg.blk0; ok && blk < blk1; ++blk) {
           if (blk < nq) {
-            const int ntile = (qn + 15) >> 4;
-#pragma unroll 1
-            for (int half = 0; half < 2; ++half) {
-              if (!(ok = tree_wait(&S.slot_empty[slot], ph, abort, p.status))) break;
-              const int t0 = blk * 8 + half * 4;
-              // lane i < 4 owns tile t0 + i; a run of tiles of one record is one copy
-              const int t = t0 + lane;
-              uint32_t bytes = 0, hbytes = 0;
-              const uint8_t* rec = nullptr;
-              int run = 0, within = 0;
-              if (lane < 4 && t < ntile) {
-                const int r = tile_record(p, t);
-                within = t - r * L.tpg;
-                if (lane == 0 || within == 0) {
-                  rec = record_addr(L, p.C, sg.b, sg.h, r, p.status);
-                  run = min(min(L.tpg - within, 4 - lane), ntile - t);
-                  if (rec) {
-                    bytes = (uint32_t)(run * L.tile_bytes);
-                    hbytes = (uint32_t)L.hdr_bytes;
-                  }
-                }
-              }
-              uint32_t okmask = rec ? (((1u << run) - 1u) << lane) : 0u;
-              okmask = __reduce_or_sync(kAll, okmask);
-              const uint32_t total = __reduce_add_sync(kAll, bytes + hbytes);
-              const uint32_t bar = smem_addr(&S.slot_full[slot]);
-              uint8_t* const dst = slots + (size_t)slot * p.slot_bytes;
-              if (lane == 0) {
-                S.slot_ok[slot] = okmask;
-                mbar_arrive_expect_tx(bar, total);
-              }
-              __syncwarp();
-              if (rec) {
-                if (hbytes) bulk_copy_g2s(smem_addr(dst + (tile_record(p, t) - tile_record(p, t0)) * 1024), rec, hbytes, bar);
-                bulk_copy_g2s(smem_addr(dst + p.slot_hdr + lane * L.tile_bytes),
-                              rec + L.hdr_bytes + (long long)within * L.tile_bytes, bytes, bar);
-              }
-              if (lane != 0) mbar_arrive(bar);
-              if (++slot == p.nslots) { slot = 0; ph ^= 1; }
-              ++used;
+            const TileMap map(p, blk);
+            const int tiles = min(8, ((qn + 15) >> 4) - map.t0);  // of this block
+            const uint32_t bar = smem_addr(&S.slot_full[slot]);
+            const uint32_t dst = smem_addr(slots + (size_t)slot * p.slot_bytes);
+            // paged: lane e owns the block's record r0 + e; contiguous: lane 0 owns all of them, one run of bytes
+            const int e = lane, first = e == 0 ? 0 : (map.r0 + e) * L.tpg - map.t0;
+            const uint8_t* rec = nullptr;
+            uint32_t bytes = 0, okmask = 0;
+            int n = 0;  // tiles that the lane copies
+            if (L.paged ? first < tiles : lane == 0) {
+              rec = record_addr(L, p.C, sg.b, sg.h, map.r0 + e, p.status);
+              n = L.paged ? min(tiles, (map.r0 + e + 1) * L.tpg - map.t0) - first : tiles;
+              const int heads = L.paged ? (e + map.own > 0) : map.record(p, tiles - 1) + map.own;
+              bytes = (uint32_t)(n * L.tile_bytes + heads * L.hdr_bytes);
+              okmask = ((1u << n) - 1u) << first;
             }
+            if (!rec) bytes = okmask = 0;
+            const bool pre = rec && e == 0 && !map.own && L.hdr_bytes;  // the header lies before the block's bytes
+            okmask = __reduce_or_sync(kAll, okmask);
+            const uint32_t total = __reduce_add_sync(kAll, bytes + (pre ? (uint32_t)L.hdr_bytes : 0u));
+            if (!(ok = tree_wait(&S.slot_empty[slot], ph, abort, p.status))) break;
+            if (lane == 0) {
+              S.slot_ok[slot] = okmask;
+              mbar_arrive_expect_tx(bar, total);
+            }
+            __syncwarp();
+            if (rec) {
+              if (pre) bulk_copy_g2s(dst, rec, L.hdr_bytes, bar);
+              const int within = e == 0 ? map.t0 - map.r0 * L.tpg : 0;
+              bulk_copy_g2s(dst + (e + map.own > 0 ? map.tile(p, first, e) - L.hdr_bytes : p.slot_hdr),
+                            rec + (within ? L.hdr_bytes + (long long)within * L.tile_bytes : 0), bytes, bar);
+            }
+            if (lane != 0) mbar_arrive(bar);
+            if (++slot == p.nslots) { slot = 0; ph ^= 1; }
+            ++used;
           } else {
             const int x0 = (blk - nq) * kBlk, n_sink = sg.n_sink;
             const int nsr = n_sink + sg.r, nrow = nsr + p.N;
@@ -696,41 +710,41 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
         const int blk1 = sg.blk1, nq = sg.nq;
         for (int blk = sg.blk0; ok && blk < blk1; ++blk) {
           const bool quant = blk < nq;
-          const int parts = quant ? 2 : kBlk / p.bf_tokens;
+          const int parts = quant ? 1 : kBlk / p.bf_tokens;
           for (int i = 0; i < parts; ++i, ++n) {
             if ((n & 1) == (uint32_t)(warp & 1)) {
               if (!(ok = tree_wait(&S.slot_full[slot], ph, abort, p.status))) break;
               if (quant) {
                 const uint32_t okmask = S.slot_ok[slot];
                 uint8_t* const src = slots + (size_t)slot * p.slot_bytes;
-                const int t0 = blk * 8 + i * 4, r0 = tile_record(p, t0);
-                const int last = 31 - __clz(okmask | 1u), nh = tile_record(p, t0 + last) - r0 + 1;
+                const TileMap map(p, blk);
+                const int nh = map.record(p, 31 - __clz(okmask | 1u)) + 1;
                 for (int e = 0; e < nh; ++e) {  // (a header whose tiles were not copied holds anything, and is not used)
-                  const float4 sc = reinterpret_cast<const float4*>(src + e * 1024)[lane];
-                  const float4 z = reinterpret_cast<const float4*>(src + e * 1024 + 512)[lane];
+                  uint8_t* const hdr = src + map.header(p, e);
+                  const float4 sc = reinterpret_cast<const float4*>(hdr)[lane];
+                  const float4 z = reinterpret_cast<const float4*>(hdr + 512)[lane];
                   const float top = fmaxf(fmaxf(group_reach(sc.x, z.x, kL), group_reach(sc.y, z.y, kL)),
                                           fmaxf(group_reach(sc.z, z.z, kL), group_reach(sc.w, z.w, kL)));
-                  // (its first tile of the slot)
-                  const int ti = e == 0 ? 0 : (r0 + e) * L.tpg - t0;
-                  if ((okmask >> ti) & 1u) worst = fmaxf(worst, top);
+                  // (its first tile of the block)
+                  if ((okmask >> (e == 0 ? 0 : (map.r0 + e) * L.tpg - map.t0)) & 1u) worst = fmaxf(worst, top);
                   __syncwarp();
-                  reinterpret_cast<uint4*>(src + e * 1024)[lane] = make_uint4(
+                  reinterpret_cast<uint4*>(hdr)[lane] = make_uint4(
                       pack_f16(sc.x, sc.y), pack_f16(sc.z, sc.w),
                       pack_f16(sc.x * (kHalf - z.x), sc.y * (kHalf - z.y)),
                       pack_f16(sc.z * (kHalf - z.z), sc.w * (kHalf - z.w)));
                 }
                 // Values: token pairs of a tile and group, 8 ngv per tile; up to 64 (whole tiles) at a time
 #pragma unroll 1
-                for (int at0 = 0; at0 < 32 * ngv; at0 += 64) {
+                for (int at0 = 0; at0 < 64 * ngv; at0 += 64) {
                   float2 sv[2], zv[2];
                   uint32_t* to[2];
 #pragma unroll
                   for (int k = 0; k < 2; ++k) {
                     const int at = at0 + k * 32 + lane, ti = at >> (3 + lg), within = at & (8 * ngv - 1);
                     const int pr = within >> lg, j = within & (ngv - 1);  // tokens 2 pr, 2 pr + 1 of group j
-                    uint8_t* const vs = src + p.slot_hdr + ti * L.tile_bytes + 32 * F::kRb;
+                    uint8_t* const vs = src + map.tile(p, ti, map.record(p, ti)) + 32 * F::kRb;
                     to[k] = nullptr;
-                    if (ti < 4 && ((okmask >> ti) & 1u)) {
+                    if (ti < 8 && ((okmask >> ti) & 1u)) {
                       const float* f = reinterpret_cast<const float*>(vs) + 2 * pr * ngv + j;
                       sv[k] = make_float2(f[0], f[ngv]);
                       zv[k] = make_float2(f[16 * ngv], f[17 * ngv]);
@@ -748,6 +762,8 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
                   }
                 }
               }
+              // (these writes come before the slot's next bulk copy)
+              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
               __syncwarp();
               if (lane == 0) mbar_arrive(smem_addr(&S.slot_ready[slot]));
             }
@@ -785,36 +801,33 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
         tc_fence_after();
         const uint32_t tt = tlane + buf * 64;
         if (blk < nq) {
+          if (!(ok = tree_wait(&ready[slot], ph, abort, p.status))) break;
+          const uint8_t* const src = slots + (size_t)slot * p.slot_bytes;
+          const uint32_t okmask = S.slot_ok[slot];
+          const TileMap map(p, blk);
+          if (!isV) {
 #pragma unroll 1
-          for (int half = 0; half < 2; ++half) {
-            if (!(ok = tree_wait(&ready[slot], ph, abort, p.status))) break;
-            const uint8_t* const src = slots + (size_t)slot * p.slot_bytes;
-            const uint32_t okmask = S.slot_ok[slot];
-            const int t0 = blk * 8 + half * 4;
-            if (!isV) {
-              if ((wq >> 1) == half) {
-#pragma unroll 1
-                for (int e = 0; e < 2; ++e) {
-                  const int ti = 2 * (wq & 1) + e;  // tile of the slot
-                  if (!((okmask >> ti) & 1u)) continue;
-                  const uint8_t* const hdr = F::kFp8 ? src : src + (tile_record(p, t0 + ti) - tile_record(p, t0)) * 1024;
-                  uint32_t w[F::kWords];
-                  load_words<FMT>(src + p.slot_hdr + ti * L.tile_bytes, lane, w);
+            for (int e = 0; e < 2; ++e) {
+              const int ti = 2 * wq + e;
+              if (!((okmask >> ti) & 1u)) continue;
+              const int rec = F::kFp8 ? 0 : map.record(p, ti);
+              const uint8_t* const hdr = F::kFp8 ? src : src + map.header(p, rec);
+              uint32_t w[F::kWords];
+              load_words<FMT>(src + (F::kFp8 ? ti * L.tile_bytes : map.tile(p, ti, rec)), lane, w);
 #pragma unroll
-                  for (int i = 0; i < 2; ++i) {
-                    uint32_t f[16];
-                    k_frags<FMT>(w, hdr, i, q, f);
-                    tc_st_frag4(tt + ((uint32_t)(16 * e) << 16) + 32 * i, f);
-                  }
-                }
+              for (int i = 0; i < 2; ++i) {
+                uint32_t f[16];
+                k_frags<FMT>(w, hdr, i, q, f);
+                tc_st_frag4(tt + ((uint32_t)(16 * e) << 16) + 32 * i, f);
               }
-            } else {
-              const uint8_t* tile = src + p.slot_hdr;
+            }
+          } else {
               // two tiles at a time, channels 32 wq .. and 32 wq + 16 ..
-              auto two = [&](int tp, uint32_t have) {
+              auto two = [&](int tp, const uint8_t* tile0, const uint8_t* tile1, uint32_t have) {
                 uint32_t f[2][8];
 #pragma unroll
-                for (int u = 0; u < 2; ++u, tile += L.tile_bytes) {
+                for (int u = 0; u < 2; ++u) {
+                  const uint8_t* const tile = u ? tile1 : tile0;
                   if (have >> u & 1u) {
                     uint32_t w[4];  // the words of steps 2 wq and 2 wq + 1
                     if constexpr (F::kBits == 8) {
@@ -836,7 +849,7 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
                     v_frag<FMT>(w + (F::kBits == 8 ? 2 : 1), 0, s1, f[1] + 4 * u);
                     if constexpr (F::kFp8) {
                       // tokens behind the last one of a partly filled tile: zeros whatever the store holds
-                      const int nv = qn - 16 * (t0 + tp + u);
+                      const int nv = qn - 16 * (map.t0 + tp + u);
                       if (nv < 16) {
                         const uint32_t m0 = pair_mask(2 * q, nv), m1 = pair_mask(2 * q + 8, nv);
 #pragma unroll
@@ -854,20 +867,19 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
                 }
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
-                  tc_st_frag2(tt + ((uint32_t)(16 * e) << 16) + 32 * half + 8 * tp, f[e]);
+                  tc_st_frag2(tt + ((uint32_t)(16 * e) << 16) + 8 * tp, f[e]);
               };
-              if (okmask == 15u) {
-                two(0, 3u);
-                two(2, 3u);
-              } else {
 #pragma unroll 1
-                for (int tp = 0; tp < 4; tp += 2) two(tp, okmask >> tp);
+              for (int tp = 0; tp < 8; tp += 2) {
+                const int o0 = F::kFp8 ? tp * L.tile_bytes : map.tile(p, tp, map.record(p, tp));
+                const int o1 = F::kFp8 ? o0 + L.tile_bytes : map.tile(p, tp + 1, map.record(p, tp + 1));
+                if (okmask == 255u) two(tp, src + o0, src + o1, 3u);
+                else two(tp, src + o0, src + o1, okmask >> tp);
               }
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_addr(&S.slot_empty[slot]));
-            if (++slot == p.nslots) { slot = 0; ph ^= 1; }
           }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_addr(&S.slot_empty[slot]));
+          if (++slot == p.nslots) { slot = 0; ph ^= 1; }
         } else {
           uint32_t top = 0;
           const bool drafts = (blk - nq) * kBlk + kBlk > sg.n_sink + sg.r;
