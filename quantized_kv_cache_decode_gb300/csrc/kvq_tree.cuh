@@ -311,17 +311,17 @@ __device__ __forceinline__ bool tree_next(const TreeParams& p, const int* pre, c
 __device__ __forceinline__ bool tree_wait(unsigned long long* bar, uint32_t parity, volatile int* abort,
                                           uint32_t* status) {
   const uint32_t a = smem_addr(bar);
-  if (mbar_try_wait(a, parity)) return true;
+  if (__builtin_expect(mbar_try_wait(a, parity), 1)) return true;
   const long long t0 = clock64();
-  while (true) {
-    if (mbar_try_wait(a, parity)) return true;
-    if (*abort) return false;
-    if (clock64() - t0 > kTreeWait) {
+  while (!mbar_try_wait(a, parity)) {
+    if (__builtin_expect(*abort != 0, 0)) return false;
+    if (__builtin_expect(clock64() - t0 > kTreeWait, 0)) {
       *abort = 1;
       report(status, KVQ_DEV_TIMEOUT);
       return false;
     }
   }
+  return true;
 }
 
 // ---------------------------------------------------------------------------
@@ -366,21 +366,21 @@ __device__ __forceinline__ uint32_t centred(const uint32_t* w, int s) {
 // s m + c with m the centred code and c = s (2^(b-1) - z).  K: 16 bytes per four channels {s01, s23, c01, c23};
 // V: per group of channels, 16 bytes per q {s of tokens 2q, 2q+1; of 2q+8, 2q+9; c of both}.
 
-// K fragments of steps 4i .. 4i+3 of a tile (rows = tokens; register pairs = channels 16s + 4q + {0,1}, {2,3})
+// K fragments of four steps of a tile from their words and scales (rows = tokens; register pairs = channels
+// 16s + 4q + {0,1}, {2,3})
 template <int FMT>
-__device__ __forceinline__ void k_frags(const uint32_t* w, const uint8_t* hdr, int i, int q, uint32_t (&r)[16]) {
+__device__ __forceinline__ void k_frags(const uint32_t* w, const uint8_t* scales, int q, uint32_t (&r)[16]) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const int s = 4 * i + j;
     if constexpr (TreeFmt<FMT>::kFp8) {
-      fp8_pairs<FMT>(w[2 * s], r[4 * j], r[4 * j + 1]);
-      fp8_pairs<FMT>(w[2 * s + 1], r[4 * j + 2], r[4 * j + 3]);
+      fp8_pairs<FMT>(w[2 * j], r[4 * j], r[4 * j + 1]);
+      fp8_pairs<FMT>(w[2 * j + 1], r[4 * j + 2], r[4 * j + 3]);
     } else {
-      const uint4 sc = *reinterpret_cast<const uint4*>(hdr + (4 * s + q) * 16);
-      r[4 * j] = hfma2(centred<FMT, 0>(w, s), sc.x, sc.z);
-      r[4 * j + 1] = hfma2(centred<FMT, 1>(w, s), sc.x, sc.z);
-      r[4 * j + 2] = hfma2(centred<FMT, 2>(w, s), sc.y, sc.w);
-      r[4 * j + 3] = hfma2(centred<FMT, 3>(w, s), sc.y, sc.w);
+      const uint4 sc = *reinterpret_cast<const uint4*>(scales + (4 * j + q) * 16);
+      r[4 * j] = hfma2(centred<FMT, 0>(w, j), sc.x, sc.z);
+      r[4 * j + 1] = hfma2(centred<FMT, 1>(w, j), sc.x, sc.z);
+      r[4 * j + 2] = hfma2(centred<FMT, 2>(w, j), sc.y, sc.w);
+      r[4 * j + 3] = hfma2(centred<FMT, 3>(w, j), sc.y, sc.w);
     }
   }
 }
@@ -403,16 +403,19 @@ __device__ __forceinline__ void v_frag(const uint32_t* w, int s, const uint4& sc
   }
 }
 
-// all operand words of the lane for one code matrix
+// the lane's operand words for steps 4i .. 4i+3 of a code matrix
 template <int FMT>
-__device__ __forceinline__ void load_words(const uint8_t* codes, int lane, uint32_t (&w)[TreeFmt<FMT>::kWords]) {
+__device__ __forceinline__ void load_words(const uint8_t* codes, int lane, int i, uint32_t (&w)[TreeFmt<FMT>::kWords / 2]) {
+  if constexpr (TreeFmt<FMT>::kBits == 2) {
+    const uint2 v = *reinterpret_cast<const uint2*>(codes + lane * 16 + i * 8);
+    w[0] = v.x, w[1] = v.y;
+  } else {
+    constexpr int kQuads = TreeFmt<FMT>::kWords / 8;
 #pragma unroll
-  for (int i = 0; i < TreeFmt<FMT>::kWords / 4; ++i) {
-    const uint4 v = *reinterpret_cast<const uint4*>(codes + (i * 32 + lane) * 16);
-    w[4 * i] = v.x;
-    w[4 * i + 1] = v.y;
-    w[4 * i + 2] = v.z;
-    w[4 * i + 3] = v.w;
+    for (int k = 0; k < kQuads; ++k) {
+      const uint4 v = *reinterpret_cast<const uint4*>(codes + ((i * kQuads + k) * 32 + lane) * 16);
+      w[4 * k] = v.x, w[4 * k + 1] = v.y, w[4 * k + 2] = v.z, w[4 * k + 3] = v.w;
+    }
   }
 }
 
@@ -744,10 +747,13 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
                     const int pr = within >> lg, j = within & (ngv - 1);  // tokens 2 pr, 2 pr + 1 of group j
                     uint8_t* const vs = src + map.tile(p, ti, map.record(p, ti)) + 32 * F::kRb;
                     to[k] = nullptr;
-                    if (ti < 8 && ((okmask >> ti) & 1u)) {
+                    sv[k] = zv[k] = make_float2(0.f, 0.f);  // (a tile that was not copied: all its Values zero)
+                    if (ti < 8) {
                       const float* f = reinterpret_cast<const float*>(vs) + 2 * pr * ngv + j;
-                      sv[k] = make_float2(f[0], f[ngv]);
-                      zv[k] = make_float2(f[16 * ngv], f[17 * ngv]);
+                      if ((okmask >> ti) & 1u) {
+                        sv[k] = make_float2(f[0], f[ngv]);
+                        zv[k] = make_float2(f[16 * ngv], f[17 * ngv]);
+                      }
                       to[k] = reinterpret_cast<uint32_t*>(vs) + j * 16 + (pr & 3) * 4 + (pr >> 2);
                     }
                   }
@@ -807,74 +813,59 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
           const TileMap map(p, blk);
           if (!isV) {
 #pragma unroll 1
-            for (int e = 0; e < 2; ++e) {
-              const int ti = 2 * wq + e;
+            for (int ei = 0; ei < 4; ++ei) {  // tile 2 wq + e, steps 4i ..
+              const int e = ei >> 1, i = ei & 1, ti = 2 * wq + e;
               if (!((okmask >> ti) & 1u)) continue;
               const int rec = F::kFp8 ? 0 : map.record(p, ti);
-              const uint8_t* const hdr = F::kFp8 ? src : src + map.header(p, rec);
-              uint32_t w[F::kWords];
-              load_words<FMT>(src + (F::kFp8 ? ti * L.tile_bytes : map.tile(p, ti, rec)), lane, w);
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                uint32_t f[16];
-                k_frags<FMT>(w, hdr, i, q, f);
-                tc_st_frag4(tt + ((uint32_t)(16 * e) << 16) + 32 * i, f);
-              }
+              uint32_t w[F::kWords / 2], f[16];
+              load_words<FMT>(src + (F::kFp8 ? ti * L.tile_bytes : map.tile(p, ti, rec)), lane, i, w);
+              k_frags<FMT>(w, F::kFp8 ? src : src + map.header(p, rec) + i * 256, q, f);
+              tc_st_frag4(tt + ((uint32_t)(16 * e) << 16) + 32 * i, f);
             }
           } else {
-              // two tiles at a time, channels 32 wq .. and 32 wq + 16 ..
-              auto two = [&](int tp, const uint8_t* tile0, const uint8_t* tile1, uint32_t have) {
+              // two tiles at a time, channels 32 wq .. and 32 wq + 16 ..  (Tiles that were not copied, behind the
+              // last one or of a bad block, read as zeros: P is 0 there, so V must be finite.)
+#pragma unroll 1
+              for (int tp = 0; tp < 8; tp += 2) {
                 uint32_t f[2][8];
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                  const uint8_t* const tile = u ? tile1 : tile0;
-                  if (have >> u & 1u) {
-                    uint32_t w[4];  // the words of steps 2 wq and 2 wq + 1
-                    if constexpr (F::kBits == 8) {
-                      const uint4 v = *reinterpret_cast<const uint4*>(tile + vcode);
-                      w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-                    } else if constexpr (F::kBits == 4) {
-                      const uint2 v = *reinterpret_cast<const uint2*>(tile + vcode);
-                      w[0] = v.x, w[1] = v.y;
-                    } else {
-                      w[0] = *reinterpret_cast<const uint32_t*>(tile + vcode);
-                      w[1] = w[0] >> 8;
-                    }
-                    uint4 s0 = make_uint4(0, 0, 0, 0), s1 = s0;  // scales of the two steps' channels
-                    if constexpr (!F::kFp8) {
-                      s0 = *reinterpret_cast<const uint4*>(tile + vs0);
-                      s1 = *reinterpret_cast<const uint4*>(tile + vs1);
-                    }
-                    v_frag<FMT>(w, 0, s0, f[0] + 4 * u);
-                    v_frag<FMT>(w + (F::kBits == 8 ? 2 : 1), 0, s1, f[1] + 4 * u);
-                    if constexpr (F::kFp8) {
-                      // tokens behind the last one of a partly filled tile: zeros whatever the store holds
-                      const int nv = qn - 16 * (map.t0 + tp + u);
-                      if (nv < 16) {
-                        const uint32_t m0 = pair_mask(2 * q, nv), m1 = pair_mask(2 * q + 8, nv);
+                  const uint8_t* const tile =
+                      src + (F::kFp8 ? (tp + u) * L.tile_bytes : map.tile(p, tp + u, map.record(p, tp + u)));
+                  uint32_t w[4];  // the words of steps 2 wq and 2 wq + 1
+                  if constexpr (F::kBits == 8) {
+                    const uint4 v = *reinterpret_cast<const uint4*>(tile + vcode);
+                    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+                  } else if constexpr (F::kBits == 4) {
+                    const uint2 v = *reinterpret_cast<const uint2*>(tile + vcode);
+                    w[0] = v.x, w[1] = v.y;
+                  } else {
+                    w[0] = *reinterpret_cast<const uint32_t*>(tile + vcode);
+                    w[1] = w[0] >> 8;
+                  }
+                  uint4 s0 = make_uint4(0, 0, 0, 0), s1 = s0;  // scales of the two steps' channels
+                  if constexpr (!F::kFp8) {
+                    s0 = *reinterpret_cast<const uint4*>(tile + vs0);
+                    s1 = *reinterpret_cast<const uint4*>(tile + vs1);
+                  }
+                  v_frag<FMT>(w, 0, s0, f[0] + 4 * u);
+                  v_frag<FMT>(w + (F::kBits == 8 ? 2 : 1), 0, s1, f[1] + 4 * u);
+                  if constexpr (F::kFp8) {
+                    // tokens behind the last one: zeros whatever the store, or an uncopied tile of the slot, holds
+                    const int nv = (okmask >> (tp + u)) & 1u ? qn - 16 * (map.t0 + tp + u) : 0;
+                    if (__builtin_expect(nv < 16, 0)) {
+                      const uint32_t m0 = pair_mask(2 * q, nv), m1 = pair_mask(2 * q + 8, nv);
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                          f[e][4 * u] &= m0, f[e][4 * u + 1] &= m0;
-                          f[e][4 * u + 2] &= m1, f[e][4 * u + 3] &= m1;
-                        }
+                      for (int e = 0; e < 2; ++e) {
+                        f[e][4 * u] &= m0, f[e][4 * u + 1] &= m0;
+                        f[e][4 * u + 2] &= m1, f[e][4 * u + 3] &= m1;
                       }
                     }
-                  } else {
-                    // not in the store (behind the last tile, or a bad block): P is 0 there, so V must be finite
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) f[e][4 * u] = f[e][4 * u + 1] = f[e][4 * u + 2] = f[e][4 * u + 3] = 0u;
                   }
                 }
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
                   tc_st_frag2(tt + ((uint32_t)(16 * e) << 16) + 8 * tp, f[e]);
-              };
-#pragma unroll 1
-              for (int tp = 0; tp < 8; tp += 2) {
-                const int o0 = F::kFp8 ? tp * L.tile_bytes : map.tile(p, tp, map.record(p, tp));
-                const int o1 = F::kFp8 ? o0 + L.tile_bytes : map.tile(p, tp + 1, map.record(p, tp + 1));
-                if (okmask == 255u) two(tp, src + o0, src + o1, 3u);
-                else two(tp, src + o0, src + o1, okmask >> tp);
               }
           }
           __syncwarp();
@@ -1045,7 +1036,7 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
         const bool quant = blk < nq;
         bool masked = false, spoilt = false;
         unsigned long long allow = ~0ull;
-        if (blk >= nplain) {
+        if (__builtin_expect(blk >= nplain, 0)) {
           bool valid;
           if (quant) {
             const int x = blk * kBlk + tok;
@@ -1071,10 +1062,25 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
           }
           masked = __any_sync(kAll, !valid);
         }
-        const float c = F::kFp8 && quant ? p.scale_log2 * S.kscale : p.scale_log2;
+        // log2 units per unit of the scores (a scale of 0 as one that no score survives: masks stay infinite)
+        float c = F::kFp8 && quant ? p.scale_log2 * S.kscale : p.scale_log2;
+        if (c == 0.f) c = 1e-37f;
         tree_wait(&S.s_full[sb], (g / Sh::kSb) & 1, abort, p.status);
         if (g > 1) tree_wait(&S.p_free[pb], ((g >> 1) - 1) & 1, abort, p.status);  // P's buffer has been read
         tc_fence_after();
+        if (masked) {  // into the scores themselves
+#pragma unroll 1
+          for (int c0 = 0; c0 < SUB; c0 += 8) {
+            const uint32_t w = (uint32_t)(allow >> c0);
+            float x[8];
+            tc_ld8(ts + c0, x);
+            tc_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = (w >> j) & 1u ? (spoilt ? NAN : x[j]) : (c > 0.f ? -INFINITY : INFINITY);
+            tc_st8(ts + c0, x);
+          }
+          tc_wait_st();
+        }
         // Columns c0 .. of the scores as exponents (log2) relative to the columns' maxima so far, and their largest
         auto exponents = [&](int c0, float (&x)[kCh], float& top) {
           float t0 = -INFINITY, t1 = -INFINITY;
@@ -1087,11 +1093,6 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
             x[j + 1] = a.y;
             x[j + 2] = b.x;
             x[j + 3] = b.y;
-          }
-          if (masked) {
-            const uint32_t w = (uint32_t)(allow >> c0);
-#pragma unroll
-            for (int j = 0; j < kCh; ++j) x[j] = (w >> j) & 1u ? (spoilt ? NAN : x[j]) : -INFINITY;
           }
 #pragma unroll
           for (int j = 0; j < kCh; j += 4) {
@@ -1113,7 +1114,7 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
         float xa[kCh], xb[kCh];
 #pragma unroll 1
         while (true) {
-          if (fresh) {
+          if (__builtin_expect(fresh, 0)) {
             // ---- the block's column maxima ----
             float top = -INFINITY;
 #pragma unroll 1
@@ -1181,7 +1182,7 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
             const bool hot = __any_sync(kAll, top > 99.f);
 #pragma unroll
             for (int j = 0; j < kCh; ++j) x[j] = exp2_approx(x[j]);
-            if (hot) {
+            if (__builtin_expect(hot, 0)) {
 #pragma unroll
               for (int j = 0; j < kCh; ++j) x[j] = fminf(x[j], kCap);
             }
@@ -1194,7 +1195,7 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
             put_p(c0, x);
             put_p(c0 + 8, x + 8);
           }
-          if (!named_any(barid, 128, top > 8.f) || again) break;
+          if (__builtin_expect(!named_any(barid, 128, top > 8.f) || again, 1)) break;
           // ---- a maximum rose by more than 8: the block over, with new maxima.  Its share is taken out of the
           // sums again (what that rounds is scaled down with them: at most 2^-24 of the new sum) ----
 #pragma unroll
