@@ -117,14 +117,6 @@ __device__ __forceinline__ float exp2_approx(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ float2 add_f32x2(float2 a, float2 b) {
-  float2 d;
-  asm("{ .reg .b64 ra, rb, rd; mov.b64 ra, {%2, %3}; mov.b64 rb, {%4, %5}; add.rn.f32x2 rd, ra, rb; "
-      "mov.b64 {%0, %1}, rd; }"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
 __device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
@@ -1019,7 +1011,7 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
       if (th < p.N && sg.blk1 > sg.nq + (sg.n_sink + sg.r) / kBlk) S.anc[th] = tree_ancestors(S.par, th);
       named_sync(3, 256);
 
-      constexpr int kCh = 16;  // columns in registers at a time
+      constexpr int kCh = SUB == 32 ? 32 : 16;  // columns in registers at a time
       float l[SUB];
 #pragma unroll
       for (int j = 0; j < SUB; ++j) l[j] = 0.f;
@@ -1081,6 +1073,11 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
           }
           tc_wait_st();
         }
+        auto load = [&](int c0, float (&x)[kCh]) {
+#pragma unroll
+          for (int j = 0; j < kCh; j += 16) tc_ld16(ts + c0 + j, x + j);
+          tc_wait_ld();
+        };
         // Columns c0 .. of the scores as exponents (log2) relative to the columns' maxima so far, and their largest
         auto exponents = [&](int c0, float (&x)[kCh], float& top) {
           float t0 = -INFINITY, t1 = -INFINITY;
@@ -1111,7 +1108,7 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
         // (a power beyond what the sums could give back is cut to kCap; its column is done over)
         constexpr float kCap = 1.2676506e30f;  // 2^100
         bool fresh = unset, again = false;     // the block's column maxima first; the pass for a second time
-        float xa[kCh], xb[kCh];
+        float x[kCh];
 #pragma unroll 1
         while (true) {
           if (__builtin_expect(fresh, 0)) {
@@ -1119,13 +1116,12 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
             float top = -INFINITY;
 #pragma unroll 1
             for (int c0 = 0; c0 < SUB; c0 += kCh) {
-              tc_ld16(ts + c0, xa);
-              tc_wait_ld();
-              exponents(c0, xa, top);
+              load(c0, x);
+              exponents(c0, x, top);
               float mine = 0.f;
 #pragma unroll
               for (int j = 0; j < kCh; ++j) {
-                const float v = warp_max(xa[j]);
+                const float v = warp_max(x[j]);
                 if (lane == j) mine = v;
               }
               if (lane < kCh) S.red[wq][h * SUB + c0 + lane] = mine;
@@ -1172,12 +1168,9 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
             if (tok == 0) S.unset[h] = 0;
           }
           float top = -INFINITY;
-          tc_ld16(ts, xa);
 #pragma unroll
           for (int c0 = 0; c0 < SUB; c0 += kCh) {
-            float(&x)[kCh] = (c0 / kCh) & 1 ? xb : xa;
-            tc_wait_ld();
-            if (c0 + kCh < SUB) tc_ld16(ts + c0 + kCh, (c0 / kCh) & 1 ? xa : xb);
+            load(c0, x);
             exponents(c0, x, top);
             const bool hot = __any_sync(kAll, top > 99.f);
 #pragma unroll
@@ -1192,19 +1185,18 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
               l[c0 + j] = n.x;
               l[c0 + j + 1] = n.y;
             }
-            put_p(c0, x);
-            put_p(c0 + 8, x + 8);
+#pragma unroll
+            for (int j = 0; j < kCh; j += 8) put_p(c0 + j, x + j);
           }
           if (__builtin_expect(!named_any(barid, 128, top > 8.f) || again, 1)) break;
           // ---- a maximum rose by more than 8: the block over, with new maxima.  Its share is taken out of the
           // sums again (what that rounds is scaled down with them: at most 2^-24 of the new sum) ----
 #pragma unroll
           for (int c0 = 0; c0 < SUB; c0 += kCh) {
-            tc_ld16(ts + c0, xa);
-            tc_wait_ld();
-            exponents(c0, xa, top);
+            load(c0, x);
+            exponents(c0, x, top);
 #pragma unroll
-            for (int j = 0; j < kCh; ++j) l[c0 + j] -= fminf(exp2_approx(xa[j]), kCap);
+            for (int j = 0; j < kCh; ++j) l[c0 + j] -= fminf(exp2_approx(x[j]), kCap);
           }
           named_sync(barid, 128);  // (the old maxima have been read)
           fresh = again = true;
