@@ -68,7 +68,6 @@ __device__ __forceinline__ long long append_row(const AppendParams& p, int b, lo
 // One CTA per (sequence, kv head): FP8 tokens (encoded one by one), bf16 rows of
 // the residual window (integer layers: only the tokens that stay there after the
 // groups that spill, which spill_kernel quantizes) and sink rows.
-template <bool PATH>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendParams p) {
   pdl_wait();  // the previous kernel of the stream has finished (programmatic launch)
   pdl_trigger();
@@ -76,10 +75,8 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
   const int b = blockIdx.x / L.H, h = blockIdx.x % L.H;
   const int tid = threadIdx.x;
   const long long pair = (long long)b * L.H + h;
-  const int n_new = append_rows<PATH>(p, b, h == 0 && tid == 0);
-  if (n_new < 0) return;
   const long long T0 = p.seq_lens[b];
-  const long long T1 = T0 + n_new;
+  const long long T1 = T0 + p.n_new;
   if (T0 < 0 || T1 > max_tokens(L)) {
     if (tid == 0) report(p.status, KVQ_DEV_CAPACITY);
     return;
@@ -110,8 +107,8 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
       }
       const int c = tid;
       const int tt = (int)(x % 16);
-      const float kx = __bfloat162float(knew[append_row<PATH>(p, b, t - T0) * L.d + c]);
-      const float vx = __bfloat162float(vnew[append_row<PATH>(p, b, t - T0) * L.d + c]);
+      const float kx = __bfloat162float(knew[(t - T0) * L.d + c]);
+      const float vx = __bfloat162float(vnew[(t - T0) * L.d + c]);
       int byte, bit;
       const float kd = __fdiv_rn(kx, sk), vd = __fdiv_rn(vx, sv);
       ktile_pos(8, true, tt, c, byte, bit);
@@ -126,15 +123,94 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
     for (long long t = rfirst; t < T1; ++t) {
       const long long slot = (t - L.S) % L.W;
       const int c = tid;
-      ring_k[(pair * L.W + slot) * L.d + c] = knew[append_row<PATH>(p, b, t - T0) * L.d + c];
-      ring_v[(pair * L.W + slot) * L.d + c] = vnew[append_row<PATH>(p, b, t - T0) * L.d + c];
+      ring_k[(pair * L.W + slot) * L.d + c] = knew[(t - T0) * L.d + c];
+      ring_v[(pair * L.W + slot) * L.d + c] = vnew[(t - T0) * L.d + c];
     }
   }
   // sink tokens
   for (long long t = T0; t < T1 && t < L.S; ++t) {
     const int c = tid;
-    sink_k[(pair * L.S + t) * L.d + c] = knew[append_row<PATH>(p, b, t - T0) * L.d + c];
-    sink_v[(pair * L.S + t) * L.d + c] = vnew[append_row<PATH>(p, b, t - T0) * L.d + c];
+    sink_k[(pair * L.S + t) * L.d + c] = knew[(t - T0) * L.d + c];
+    sink_v[(pair * L.S + t) * L.d + c] = vnew[(t - T0) * L.d + c];
+  }
+}
+
+// kvq_append_accepted of FP8 and bf16 layers.  One CTA per (sequence, kv head), 128 threads a token (thread = channel),
+// four tokens at a time and the loads of up to sixteen before the first store: a path is a few tokens, so the call is a
+// chain of dependent steps (lengths, path, rows, codes) and costs what their latencies add up to.
+constexpr int kPathTokens = 4, kPathBatch = 4;
+__global__ void __launch_bounds__(128 * kPathTokens) append_path_kernel(const AppendParams p) {
+  __shared__ int rows[kMaxNodes];
+  pdl_wait();
+  pdl_trigger();
+  const LayerDesc& L = p.L;
+  const int b = blockIdx.x / L.H, h = blockIdx.x - b * L.H;
+  const int tid = threadIdx.x, c = tid & 127, sub = tid >> 7;
+  const long long pair = (long long)b * L.H + h;
+  const int n = p.counts[b];
+  const long long T0 = p.seq_lens[b];
+  const float sk = L.fp8 ? *p.C.k_tscale : 1.f, sv = L.fp8 ? *p.C.v_tscale : 1.f;
+  bool bad = n < 0 || n > p.n_new;
+  if (tid < p.n_new && tid < n) {
+    const int r = p.path[(long long)b * p.n_new + tid];
+    bad |= r < 0 || r >= p.n_new;
+    rows[tid] = r;
+  }
+  if (__syncthreads_or(bad)) {
+    if (h == 0 && tid == 0) report(p.status, KVQ_DEV_BAD_TREE);
+    return;
+  }
+  if (T0 < 0 || T0 + n > max_tokens(L)) {
+    if (tid == 0) report(p.status, KVQ_DEV_CAPACITY);
+    return;
+  }
+  const __nv_bfloat16* knew = reinterpret_cast<const __nv_bfloat16*>(p.k_new) + pair * p.n_new * L.d + c;
+  const __nv_bfloat16* vnew = reinterpret_cast<const __nv_bfloat16*>(p.v_new) + pair * p.n_new * L.d + c;
+  for (int j0 = 0; j0 < n; j0 += kPathTokens * kPathBatch) {
+    __nv_bfloat16 k[kPathBatch], v[kPathBatch];
+#pragma unroll
+    for (int i = 0; i < kPathBatch; ++i) {
+      const int j = j0 + i * kPathTokens + sub;
+      if (j < n) {
+        k[i] = knew[(long long)rows[j] * L.d];
+        v[i] = vnew[(long long)rows[j] * L.d];
+      }
+    }
+    if (L.fp8 && j0 == 0) {
+      // tiles that begin here: cleared, so that the codes of tokens not yet written read as 0
+      const unsigned x0 = T0 > L.S ? (unsigned)(T0 - L.S) : 0u, x1 = T0 + n > L.S ? (unsigned)(T0 + n - L.S) : 0u;
+      for (unsigned i = (x0 + 15) / 16; i * 16 < x1; ++i) {
+        uint8_t* rec = record_w(L, p.C, b, h, i / (unsigned)L.tpg, nullptr);  // (reported below)
+        if (rec)
+          for (int w = tid; w < 2 * L.rb; w += 128 * kPathTokens)
+            reinterpret_cast<uint4*>(rec + (long long)(i % (unsigned)L.tpg) * L.tile_bytes)[w] = make_uint4(0u, 0u, 0u, 0u);
+      }
+      __syncthreads();
+    }
+#pragma unroll
+    for (int i = 0; i < kPathBatch; ++i) {
+      const int j = j0 + i * kPathTokens + sub;
+      if (j >= n) continue;
+      const long long t = T0 + j;
+      if (t < L.S) {
+        reinterpret_cast<__nv_bfloat16*>(p.C.sink_k)[(pair * L.S + t) * L.d + c] = k[i];
+        reinterpret_cast<__nv_bfloat16*>(p.C.sink_v)[(pair * L.S + t) * L.d + c] = v[i];
+      } else if (L.bf16) {  // row t - S: the buffers never wrap
+        reinterpret_cast<__nv_bfloat16*>(p.C.resid_k)[(pair * L.W + (t - L.S)) * L.d + c] = k[i];
+        reinterpret_cast<__nv_bfloat16*>(p.C.resid_v)[(pair * L.W + (t - L.S)) * L.d + c] = v[i];
+      } else {
+        const unsigned x = (unsigned)(t - L.S), ti = x / 16;
+        uint8_t* rec = record_w(L, p.C, b, h, ti / (unsigned)L.tpg, c == 0 ? p.status : nullptr);
+        if (!rec) continue;
+        uint8_t* tile = rec + (long long)(ti % (unsigned)L.tpg) * L.tile_bytes;
+        const float kd = __fdiv_rn(__bfloat162float(k[i]), sk), vd = __fdiv_rn(__bfloat162float(v[i]), sv);
+        int byte, bit;
+        ktile_pos(8, true, (int)(x % 16), c, byte, bit);
+        tile[byte] = L.e5m2 ? f32_to_e5m2(kd) : f32_to_e4m3(kd);
+        vtile_pos(8, true, (int)(x % 16), c, byte, bit);
+        tile[16 * L.rb + byte] = L.e5m2 ? f32_to_e5m2(vd) : f32_to_e4m3(vd);
+      }
+    }
   }
 }
 
@@ -486,8 +562,8 @@ cudaError_t launch_append(const AppendParams& p, cudaStream_t stream) {
   const int blocks = p.batch * p.L.H;
   if (blocks == 0 || p.n_new == 0) return cudaSuccess;
   if (p.L.fp8 || p.L.bf16) {
-    return p.path ? launch_pdl(append_kernel<true>, dim3(blocks), dim3(kAppendThreads), 0, stream, p)
-                  : launch_pdl(append_kernel<false>, dim3(blocks), dim3(kAppendThreads), 0, stream, p);
+    return p.path ? launch_pdl(append_path_kernel, dim3(blocks), dim3(128 * kPathTokens), 0, stream, p)
+                  : launch_pdl(append_kernel, dim3(blocks), dim3(kAppendThreads), 0, stream, p);
   }
   if (p.path) return launch_spill<true>(p, 1, 1, stream);  // spills, window and sink rows in one launch
   // integer layers: at most ceil(n_new / G) groups spill per (sequence, head)
@@ -495,7 +571,7 @@ cudaError_t launch_append(const AppendParams& p, cudaStream_t stream) {
   const int fused = p.n_new == 1;  // one new token: its row never aliases a ring row the spill reads
   const cudaError_t e = launch_spill<false>(p, groups, fused, stream);
   if (e != cudaSuccess || fused) return e;
-  return launch_pdl(append_kernel<false>, dim3(blocks), dim3(kAppendThreads), 0, stream, p);  // window and sink rows after the spills
+  return launch_pdl(append_kernel, dim3(blocks), dim3(kAppendThreads), 0, stream, p);  // window and sink rows after the spills
 }
 
 // ---------------------------------------------------------------------------
