@@ -197,6 +197,7 @@ struct TreeSmem {  // small shared state, after the big buffers
   unsigned long long slot_full[kMaxSlots], slot_ready[kMaxSlots], slot_empty[kMaxSlots];
   unsigned long long k_full[2], k_empty[2], v_full[2], v_empty[2];
   unsigned long long s_full[2], s_free[2], p_full[2], p_free[2], q_full, drain;
+  int tile_at[kMaxSlots][8], head_at[kMaxSlots][8];  // integer layers: byte offsets of a slot's tiles, of their Key scales
   uint32_t slot_ok[kMaxSlots];  // quantized slots: which of the four tiles were copied
   uint32_t tmem;
   int abort;
@@ -414,6 +415,11 @@ __device__ __forceinline__ void load_words(const uint8_t* codes, int lane, int i
 // largest magnitude that a group of scale s and zero point z stands for
 __device__ __forceinline__ float group_reach(float s, float z, float levels) {
   return fabsf(s) * fmaxf(fabsf(z), fabsf(levels - z));
+}
+// whether one of four groups may stand for more than f16 holds (s m + c with |m| <= half)
+__device__ __forceinline__ bool beyond_f16(const float4& s, const float4& c, float half) {
+  return fmaxf(fmaxf(fmaf(fabsf(s.x), half, fabsf(c.x)), fmaf(fabsf(s.y), half, fabsf(c.y))),
+               fmaxf(fmaf(fabsf(s.z), half, fabsf(c.z)), fmaf(fabsf(s.w), half, fabsf(c.w)))) >= 65000.f;
 }
 // f16 pair of tokens t, t + 1: all ones where the token is below n
 __device__ __forceinline__ uint32_t pair_mask(int t, int n) {
@@ -714,50 +720,44 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
                 uint8_t* const src = slots + (size_t)slot * p.slot_bytes;
                 const TileMap map(p, blk);
                 const int nh = map.record(p, 31 - __clz(okmask | 1u)) + 1;
+                // where the dequantization finds the tiles and their Key scales
+                if (lane < 8) {
+                  const int e = map.record(p, lane);
+                  S.tile_at[slot][lane] = map.tile(p, lane, e);
+                  S.head_at[slot][lane] = map.header(p, e);
+                }
+#pragma unroll 1
                 for (int e = 0; e < nh; ++e) {  // (a header whose tiles were not copied holds anything, and is not used)
                   uint8_t* const hdr = src + map.header(p, e);
                   const float4 sc = reinterpret_cast<const float4*>(hdr)[lane];
                   const float4 z = reinterpret_cast<const float4*>(hdr + 512)[lane];
-                  const float top = fmaxf(fmaxf(group_reach(sc.x, z.x, kL), group_reach(sc.y, z.y, kL)),
-                                          fmaxf(group_reach(sc.z, z.z, kL), group_reach(sc.w, z.w, kL)));
-                  // (its first tile of the block)
-                  if ((okmask >> (e == 0 ? 0 : (map.r0 + e) * L.tpg - map.t0)) & 1u) worst = fmaxf(worst, top);
+                  const float4 c = make_float4(sc.x * (kHalf - z.x), sc.y * (kHalf - z.y), sc.z * (kHalf - z.z), sc.w * (kHalf - z.w));
+                  const int ti = e == 0 ? 0 : (map.r0 + e) * L.tpg - map.t0;  // its first tile of the block
+                  if (beyond_f16(sc, c, kHalf) && ((okmask >> ti) & 1u))
+                    worst = fmaxf(worst, fmaxf(fmaxf(group_reach(sc.x, z.x, kL), group_reach(sc.y, z.y, kL)),
+                                               fmaxf(group_reach(sc.z, z.z, kL), group_reach(sc.w, z.w, kL))));
                   __syncwarp();
-                  reinterpret_cast<uint4*>(hdr)[lane] = make_uint4(
-                      pack_f16(sc.x, sc.y), pack_f16(sc.z, sc.w),
-                      pack_f16(sc.x * (kHalf - z.x), sc.y * (kHalf - z.y)),
-                      pack_f16(sc.z * (kHalf - z.z), sc.w * (kHalf - z.w)));
+                  reinterpret_cast<uint4*>(hdr)[lane] =
+                      make_uint4(pack_f16(sc.x, sc.y), pack_f16(sc.z, sc.w), pack_f16(c.x, c.y), pack_f16(c.z, c.w));
                 }
-                // Values: token pairs of a tile and group, 8 ngv per tile; up to 64 (whole tiles) at a time
+                // Values: a lane per (tile, q, group), the tokens 2q, 2q + 1, 2q + 8, 2q + 9; whole tiles at a time
 #pragma unroll 1
-                for (int at0 = 0; at0 < 64 * ngv; at0 += 64) {
-                  float2 sv[2], zv[2];
-                  uint32_t* to[2];
-#pragma unroll
-                  for (int k = 0; k < 2; ++k) {
-                    const int at = at0 + k * 32 + lane, ti = at >> (3 + lg), within = at & (8 * ngv - 1);
-                    const int pr = within >> lg, j = within & (ngv - 1);  // tokens 2 pr, 2 pr + 1 of group j
-                    uint8_t* const vs = src + map.tile(p, ti, map.record(p, ti)) + 32 * F::kRb;
-                    to[k] = nullptr;
-                    sv[k] = zv[k] = make_float2(0.f, 0.f);  // (a tile that was not copied: all its Values zero)
-                    if (ti < 8) {
-                      const float* f = reinterpret_cast<const float*>(vs) + 2 * pr * ngv + j;
-                      if ((okmask >> ti) & 1u) {
-                        sv[k] = make_float2(f[0], f[ngv]);
-                        zv[k] = make_float2(f[16 * ngv], f[17 * ngv]);
-                      }
-                      to[k] = reinterpret_cast<uint32_t*>(vs) + j * 16 + (pr & 3) * 4 + (pr >> 2);
-                    }
+                for (int at = lane; at < 32 * ngv; at += 32) {
+                  const int ti = at >> (2 + lg), within = at & (4 * ngv - 1), vq = within >> lg, j = within & (ngv - 1);
+                  uint8_t* const to = src + map.tile(p, ti, map.record(p, ti)) + 32 * F::kRb;
+                  const float* const f = reinterpret_cast<const float*>(to) + 2 * vq * ngv + j;
+                  uint4 out = make_uint4(0u, 0u, 0u, 0u);  // (a tile that was not copied: all its Values zero)
+                  if ((okmask >> ti) & 1u) {
+                    const float4 sc = make_float4(f[0], f[ngv], f[8 * ngv], f[9 * ngv]);
+                    const float4 z = make_float4(f[16 * ngv], f[17 * ngv], f[24 * ngv], f[25 * ngv]);
+                    const float4 c = make_float4(sc.x * (kHalf - z.x), sc.y * (kHalf - z.y), sc.z * (kHalf - z.z), sc.w * (kHalf - z.w));
+                    if (beyond_f16(sc, c, kHalf))
+                      worst = fmaxf(worst, fmaxf(fmaxf(group_reach(sc.x, z.x, kL), group_reach(sc.y, z.y, kL)),
+                                                 fmaxf(group_reach(sc.z, z.z, kL), group_reach(sc.w, z.w, kL))));
+                    out = make_uint4(pack_f16(sc.x, sc.y), pack_f16(sc.z, sc.w), pack_f16(c.x, c.y), pack_f16(c.z, c.w));
                   }
                   __syncwarp();
-#pragma unroll
-                  for (int k = 0; k < 2; ++k) {
-                    if (to[k]) {
-                      worst = fmaxf(worst, fmaxf(group_reach(sv[k].x, zv[k].x, kL), group_reach(sv[k].y, zv[k].y, kL)));
-                      to[k][0] = pack_f16(sv[k].x, sv[k].y);
-                      to[k][2] = pack_f16(sv[k].x * (kHalf - zv[k].x), sv[k].y * (kHalf - zv[k].y));
-                    }
-                  }
+                  *reinterpret_cast<uint4*>(to + j * 64 + vq * 16) = out;
                 }
               }
               // (these writes come before the slot's next bulk copy)
@@ -802,16 +802,14 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
           if (!(ok = tree_wait(&ready[slot], ph, abort, p.status))) break;
           const uint8_t* const src = slots + (size_t)slot * p.slot_bytes;
           const uint32_t okmask = S.slot_ok[slot];
-          const TileMap map(p, blk);
           if (!isV) {
 #pragma unroll 1
             for (int ei = 0; ei < 4; ++ei) {  // tile 2 wq + e, steps 4i ..
               const int e = ei >> 1, i = ei & 1, ti = 2 * wq + e;
               if (!((okmask >> ti) & 1u)) continue;
-              const int rec = F::kFp8 ? 0 : map.record(p, ti);
               uint32_t w[F::kWords / 2], f[16];
-              load_words<FMT>(src + (F::kFp8 ? ti * L.tile_bytes : map.tile(p, ti, rec)), lane, i, w);
-              k_frags<FMT>(w, F::kFp8 ? src : src + map.header(p, rec) + i * 256, q, f);
+              load_words<FMT>(src + (F::kFp8 ? ti * L.tile_bytes : S.tile_at[slot][ti]), lane, i, w);
+              k_frags<FMT>(w, F::kFp8 ? src : src + S.head_at[slot][ti] + i * 256, q, f);
               tc_st_frag4(tt + ((uint32_t)(16 * e) << 16) + 32 * i, f);
             }
           } else {
@@ -822,8 +820,7 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
                 uint32_t f[2][8];
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                  const uint8_t* const tile =
-                      src + (F::kFp8 ? (tp + u) * L.tile_bytes : map.tile(p, tp + u, map.record(p, tp + u)));
+                  const uint8_t* const tile = src + (F::kFp8 ? (tp + u) * L.tile_bytes : S.tile_at[slot][tp + u]);
                   uint32_t w[4];  // the words of steps 2 wq and 2 wq + 1
                   if constexpr (F::kBits == 8) {
                     const uint4 v = *reinterpret_cast<const uint4*>(tile + vcode);
@@ -844,7 +841,7 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
                   v_frag<FMT>(w + (F::kBits == 8 ? 2 : 1), 0, s1, f[1] + 4 * u);
                   if constexpr (F::kFp8) {
                     // tokens behind the last one: zeros whatever the store, or an uncopied tile of the slot, holds
-                    const int nv = (okmask >> (tp + u)) & 1u ? qn - 16 * (map.t0 + tp + u) : 0;
+                    const int nv = (okmask >> (tp + u)) & 1u ? qn - 16 * (8 * blk + tp + u) : 0;
                     if (__builtin_expect(nv < 16, 0)) {
                       const uint32_t m0 = pair_mask(2 * q, nv), m1 = pair_mask(2 * q + 8, nv);
 #pragma unroll
