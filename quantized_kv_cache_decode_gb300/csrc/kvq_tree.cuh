@@ -53,7 +53,19 @@ __device__ __forceinline__ void tc_relinquish() {
 }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// The loads' registers pass through the wait, so that nothing reads them before it.
+__device__ __forceinline__ void tc_wait_ld(float (&x)[8]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(x[0]), "+f"(x[1]), "+f"(x[2]), "+f"(x[3]), "+f"(x[4]), "+f"(x[5]), "+f"(x[6]), "+f"(x[7])
+               :
+               : "memory");
+}
+template <int N>
+__device__ __forceinline__ void tc_wait_ld(float (&x)[N]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+f"(x[i]));
+}
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tc_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
@@ -65,19 +77,21 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, ui
       "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// 16 lanes x 16 columns in fragment order: four 16 x 16 f16 fragments (4 registers each) side by side
-__device__ __forceinline__ void tc_st_frag4(uint32_t taddr, const uint32_t (&r)[16]) {
+// 16 lanes in fragment order: four, two or one 16 x 16 f16 fragments (4 registers each) side by side
+__device__ __forceinline__ void tc_st_frags(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
           taddr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]));
 }
-__device__ __forceinline__ void tc_st_frag2(uint32_t taddr, const uint32_t (&r)[8]) {
+__device__ __forceinline__ void tc_st_frags(uint32_t taddr, const uint32_t (&r)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]));
+}
+__device__ __forceinline__ void tc_st_frags(uint32_t taddr, const uint32_t (&r)[8]) {
   asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
-               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-               : "memory");
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]));
 }
 // 32 lanes x 16 columns, one lane per thread
 __device__ __forceinline__ void tc_ld16(uint32_t taddr, float* x) {
@@ -97,8 +111,7 @@ __device__ __forceinline__ void tc_ld8(uint32_t taddr, float* x) {
 __device__ __forceinline__ void tc_st8(uint32_t taddr, const float* x) {
   const uint32_t* u = reinterpret_cast<const uint32_t*>(x);
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(u[0]),
-               "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
-               : "memory");
+               "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]));
 }
 
 // Shared-memory matrix descriptor: start address, leading and stride byte offsets (16-byte
@@ -155,13 +168,16 @@ constexpr int kBlk = 128;  // cache tokens per block
 
 template <int NT>
 struct TreeShape {
-  static constexpr int kSub = NT / 2;              // columns of a softmax warpgroup
-  static constexpr int kWarps = 20;                // 4 K, 4 V, 8 softmax, then loader, MMA, check, (idle)
-  static constexpr int kThreads = 32 * kWarps;
+  // warps: 4 K, 4 V, then a softmax warpgroup per kSub columns, then loader, MMA, two prep warps.  128 columns take
+  // four softmax warpgroups (two of 64 columns each leave a scheduler too few warps to issue from: a 70B-shaped
+  // INT4 layer 152 -> 105 us), whose registers leave the others few
+  static constexpr int kGroups = NT == 128 ? 4 : 2, kSub = NT / kGroups;
+  static constexpr int kSmWarps = 4 * kGroups, kIo = 8 + kSmWarps;
+  static constexpr int kWarps = kIo + 4, kThreads = 32 * kWarps;
   // registers a thread: at launch, then by role (the roles' warpgroups together stay within the launch's)
-  static constexpr int kRegLaunch = 96;
-  static constexpr int kRegDq = NT == 128 ? 80 : 88, kRegSm = NT == 128 ? 136 : 128, kRegIo = 48;
-  static_assert(2 * kRegDq + 2 * kRegSm + kRegIo <= 5 * kRegLaunch, "register split");
+  static constexpr int kRegLaunch = NT == 128 ? 72 : 96;
+  static constexpr int kRegDq = NT == 128 ? 56 : 80, kRegSm = NT == 128 ? 88 : 128, kRegIo = NT == 128 ? 40 : 64;
+  static_assert(2 * kRegDq + kGroups * kRegSm + kRegIo <= (kWarps / 4) * kRegLaunch, "register split");
   static constexpr int kQBytes = NT * 256;         // queries (f16): [two 64-channel halves][NT rows of 128 bytes]
   static constexpr int kPBytes = kBlk * NT * 2;    // one buffer of P (f16)
   static constexpr int kFixed = kQBytes + 2 * kPBytes;
@@ -206,15 +222,15 @@ struct TreeSmem {  // small shared state, after the big buffers
   alignas(16) float fall[128];    // what a change of the maxima scales sums by; epilogue: 1 / sum
   alignas(16) float red[4][128];  // the four warps' maxima or sums
   int row[128];                   // epilogue: the columns' rows of the output, -1: none
-  int unset[2];
+  int unset[4];
   unsigned long long anc[64];     // a node's ancestors and itself
   unsigned long long wild;        // nodes whose drafted Values f16 does not hold
   int par[64];
   unsigned units, ctas;           // blocks of the launch, CTAs that share them
   float kscale, vunit;            // FP8: the Keys' tensor scale, the unit of the Values (else 1)
   int least, most;                // blocks of the shortest and the longest sequence
-  TreeCursor cur[20];             // per warp
-  TreeSeg seg[20];
+  TreeCursor cur[28];             // per warp
+  TreeSeg seg[28];
 };
 
 // node n's ancestors and itself; par[n] < n, or -1
@@ -359,17 +375,17 @@ __device__ __forceinline__ uint32_t centred(const uint32_t* w, int s) {
 // s m + c with m the centred code and c = s (2^(b-1) - z).  K: 16 bytes per four channels {s01, s23, c01, c23};
 // V: per group of channels, 16 bytes per q {s of tokens 2q, 2q+1; of 2q+8, 2q+9; c of both}.
 
-// K fragments of four steps of a tile from their words and scales (rows = tokens; register pairs = channels
+// K fragments of N steps of a tile from their words and scales (rows = tokens; register pairs = channels
 // 16s + 4q + {0,1}, {2,3})
-template <int FMT>
-__device__ __forceinline__ void k_frags(const uint32_t* w, const uint8_t* scales, int q, uint32_t (&r)[16]) {
+template <int FMT, int N>
+__device__ __forceinline__ void k_frags(const uint32_t* w, const uint4* scales, uint32_t (&r)[4 * N]) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
+  for (int j = 0; j < N; ++j) {
     if constexpr (TreeFmt<FMT>::kFp8) {
       fp8_pairs<FMT>(w[2 * j], r[4 * j], r[4 * j + 1]);
       fp8_pairs<FMT>(w[2 * j + 1], r[4 * j + 2], r[4 * j + 3]);
     } else {
-      const uint4 sc = *reinterpret_cast<const uint4*>(scales + (4 * j + q) * 16);
+      const uint4 sc = scales[j];
       r[4 * j] = hfma2(centred<FMT, 0>(w, j), sc.x, sc.z);
       r[4 * j + 1] = hfma2(centred<FMT, 1>(w, j), sc.x, sc.z);
       r[4 * j + 2] = hfma2(centred<FMT, 2>(w, j), sc.y, sc.w);
@@ -396,19 +412,22 @@ __device__ __forceinline__ void v_frag(const uint32_t* w, int s, const uint4& sc
   }
 }
 
-// the lane's operand words for steps 4i .. 4i+3 of a code matrix
-template <int FMT>
-__device__ __forceinline__ void load_words(const uint8_t* codes, int lane, int i, uint32_t (&w)[TreeFmt<FMT>::kWords / 2]) {
-  if constexpr (TreeFmt<FMT>::kBits == 2) {
-    const uint2 v = *reinterpret_cast<const uint2*>(codes + lane * 16 + i * 8);
-    w[0] = v.x, w[1] = v.y;
-  } else {
-    constexpr int kQuads = TreeFmt<FMT>::kWords / 8;
+// the lane's operand words for steps N i .. N i + N - 1 of a code matrix (word w of a lane lies at byte
+// ((w / 4) * 32 + lane) * 16 + (w % 4) * 4)
+template <int FMT, int N>
+__device__ __forceinline__ void load_words(const uint8_t* codes, int lane, int i, uint32_t (&w)[N * TreeFmt<FMT>::kWords / 8]) {
+  constexpr int kN = N * TreeFmt<FMT>::kWords / 8;  // 1, 2, 4 or 8
+  if constexpr (kN >= 4) {
 #pragma unroll
-    for (int k = 0; k < kQuads; ++k) {
-      const uint4 v = *reinterpret_cast<const uint4*>(codes + ((i * kQuads + k) * 32 + lane) * 16);
+    for (int k = 0; k < kN / 4; ++k) {
+      const uint4 v = *reinterpret_cast<const uint4*>(codes + ((i * (kN / 4) + k) * 32 + lane) * 16);
       w[4 * k] = v.x, w[4 * k + 1] = v.y, w[4 * k + 2] = v.z, w[4 * k + 3] = v.w;
     }
+  } else if constexpr (kN == 2) {
+    const uint2 v = *reinterpret_cast<const uint2*>(codes + ((i >> 1) * 32 + lane) * 16 + (i & 1) * 8);
+    w[0] = v.x, w[1] = v.y;
+  } else {
+    w[0] = *reinterpret_cast<const uint32_t*>(codes + lane * 16 + i * 4);
   }
 }
 
@@ -480,17 +499,17 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
       mbar_init(smem_addr(&S.v_full[i]), 4);
       mbar_init(smem_addr(&S.v_empty[i]), 1);
       mbar_init(smem_addr(&S.s_full[i]), 1);
-      mbar_init(smem_addr(&S.s_free[i]), 8);
-      mbar_init(smem_addr(&S.p_full[i]), 8);
+      mbar_init(smem_addr(&S.s_free[i]), Sh::kSmWarps);
+      mbar_init(smem_addr(&S.p_full[i]), Sh::kSmWarps);
       mbar_init(smem_addr(&S.p_free[i]), 1);
     }
-    mbar_init(smem_addr(&S.q_full), 8);
+    mbar_init(smem_addr(&S.q_full), Sh::kSmWarps);
     mbar_init(smem_addr(&S.drain), 1);
     S.abort = 0;
-    S.unset[0] = S.unset[1] = 0;
+    for (int i = 0; i < 4; ++i) S.unset[i] = 0;
     fence_barrier_init();
   }
-  if (warp == 17) {
+  if (warp == Sh::kIo + 1) {
     tc_alloc512(smem_addr(&S.tmem));
     tc_relinquish();
   }
@@ -549,9 +568,9 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
   __syncwarp();
 
   // (each role's branch begins with its register count, which the compiler then allocates by)
-  if (warp >= 16) {
+  if (warp >= Sh::kIo) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Sh::kRegIo));
-    if (warp == 16) {
+    if (warp == Sh::kIo) {
       // ======================= loader =======================
       int slot = 0;
       uint32_t ph = 1;  // the first pass over the slots finds them empty
@@ -644,7 +663,7 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
           mbar_wait_bounded(smem_addr(&S.slot_full[n % p.nslots]), (n / p.nslots) & 1, kTreeWait);
         }
       }
-    } else if (warp == 17) {
+    } else if (warp == Sh::kIo + 1) {
       // ======================= MMA =======================
       // (the whole warp walks, so that the operands of the one-thread instructions stay uniform)
       constexpr uint32_t kIdQk = mma_idesc(NT, 0), kIdPv = mma_idesc(NT, 1);
@@ -781,6 +800,8 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
     unsigned long long* const full = isV ? S.v_full : S.k_full;
     unsigned long long* const empty = isV ? S.v_empty : S.k_empty;
     unsigned long long* const ready = F::kFp8 ? S.slot_full : S.slot_ready;
+    // fragments in registers at a time (K: steps of a tile; V: tiles)
+    constexpr int kSteps = NT == 128 ? 2 : 4, kTiles = NT == 128 ? 1 : 2;
     int slot = 0;
     uint32_t ph = 0, g = 0;
     bool ok = true, bad = false;
@@ -803,23 +824,35 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
           const uint8_t* const src = slots + (size_t)slot * p.slot_bytes;
           const uint32_t okmask = S.slot_ok[slot];
           if (!isV) {
-#pragma unroll 1
-            for (int ei = 0; ei < 4; ++ei) {  // tile 2 wq + e, steps 4i ..
-              const int e = ei >> 1, i = ei & 1, ti = 2 * wq + e;
-              if (!((okmask >> ti) & 1u)) continue;
-              uint32_t w[F::kWords / 2], f[16];
-              load_words<FMT>(src + (F::kFp8 ? ti * L.tile_bytes : S.tile_at[slot][ti]), lane, i, w);
-              k_frags<FMT>(w, F::kFp8 ? src : src + S.head_at[slot][ti] + i * 256, q, f);
-              tc_st_frag4(tt + ((uint32_t)(16 * e) << 16) + 32 * i, f);
+            // tile 2 wq + e, kSteps steps at a time; the next ones' words and scales on their way meanwhile
+            constexpr int kPer = 8 / kSteps;
+            uint32_t w[2][kSteps * F::kWords / 8];
+            uint4 sc[2][kSteps];
+            auto fetch = [&](int ei, int to) {
+              const int ti = 2 * wq + ei / kPer, i = ei % kPer;
+              load_words<FMT, kSteps>(src + (F::kFp8 ? ti * L.tile_bytes : S.tile_at[slot][ti]), lane, i, w[to]);
+              if constexpr (!F::kFp8) {
+                const uint4* const s = reinterpret_cast<const uint4*>(src + S.head_at[slot][ti]) + 4 * kSteps * i + q;
+#pragma unroll
+                for (int j = 0; j < kSteps; ++j) sc[to][j] = s[4 * j];
+              }
+            };
+            fetch(0, 0);
+#pragma unroll 2
+            for (int ei = 0; ei < 2 * kPer; ++ei) {
+              if (ei + 1 < 2 * kPer) fetch(ei + 1, (ei + 1) & 1);
+              uint32_t f[4 * kSteps];
+              k_frags<FMT, kSteps>(w[ei & 1], sc[ei & 1], f);
+              tc_st_frags(tt + ((uint32_t)(16 * (ei / kPer)) << 16) + 8 * kSteps * (ei % kPer), f);
             }
           } else {
-              // two tiles at a time, channels 32 wq .. and 32 wq + 16 ..  (Tiles that were not copied, behind the
+              // kTiles tiles at a time, channels 32 wq .. and 32 wq + 16 ..  (Tiles that were not copied, behind the
               // last one or of a bad block, read as zeros: P is 0 there, so V must be finite.)
-#pragma unroll 1
-              for (int tp = 0; tp < 8; tp += 2) {
-                uint32_t f[2][8];
+#pragma unroll 2
+              for (int tp = 0; tp < 8; tp += kTiles) {
+                uint32_t f[2][4 * kTiles];
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
+                for (int u = 0; u < kTiles; ++u) {
                   const uint8_t* const tile = src + (F::kFp8 ? (tp + u) * L.tile_bytes : S.tile_at[slot][tp + u]);
                   uint32_t w[4];  // the words of steps 2 wq and 2 wq + 1
                   if constexpr (F::kBits == 8) {
@@ -854,7 +887,7 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
                 }
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
-                  tc_st_frag2(tt + ((uint32_t)(16 * e) << 16) + 8 * tp, f[e]);
+                  tc_st_frags(tt + ((uint32_t)(16 * e) << 16) + 8 * tp, f[e]);
               }
           }
           __syncwarp();
@@ -871,13 +904,13 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
             if (!isV) {
               if (32 * wq >= part && 32 * wq < part + p.bf_tokens) {
 #pragma unroll 1
-                for (int ei = 0; ei < 4; ++ei) {  // 16 rows, four steps
-                  const int e = ei >> 1, i = ei & 1;
+                for (int ei = 0; ei < 16 / kSteps; ++ei) {  // 16 rows, kSteps steps
+                  const int e = ei / (8 / kSteps), i = ei % (8 / kSteps);
                   const int row = 32 * wq - part + 16 * e + r;
-                  uint32_t f[16];
+                  uint32_t f[4 * kSteps];
 #pragma unroll
-                  for (int j = 0; j < 4; ++j) {
-                    const int c = 2 * (4 * i + j) + (q >> 1);
+                  for (int j = 0; j < kSteps; ++j) {
+                    const int c = 2 * (kSteps * i + j) + (q >> 1);
                     const uint2 a = *reinterpret_cast<const uint2*>(src + krow_chunk(row, c) + (q & 1) * 8);
                     const uint2 b = *reinterpret_cast<const uint2*>(src + krow_chunk(row + 8, c) + (q & 1) * 8);
                     top = abs_max2(abs_max2(abs_max2(abs_max2(top, a.x), a.y), b.x), b.y);
@@ -886,20 +919,20 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
                     f[4 * j + 2] = bf16x2_to_f16x2(a.y);
                     f[4 * j + 3] = bf16x2_to_f16x2(b.y);
                   }
-                  tc_st_frag4(tt + ((uint32_t)(16 * e) << 16) + 32 * i, f);
+                  tc_st_frags(tt + ((uint32_t)(16 * e) << 16) + 8 * kSteps * i, f);
                 }
               }
             } else {
               const uint32_t vbase = smem_addr(src) + p.bf_tokens * 256;
               const int row0 = (lane & 7) + ((lane >> 4) << 3), cc = (lane >> 3) & 1;
 #pragma unroll 1
-              for (int t4 = 0; t4 < p.bf_tokens; t4 += 32) {  // two fragments of 16 tokens at a time
+              for (int t4 = 0; t4 < p.bf_tokens; t4 += 16 * kTiles) {  // kTiles fragments of 16 tokens at a time
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                   const int c = 2 * (2 * wq + e) + cc;
-                  uint32_t f[8];
+                  uint32_t f[4 * kTiles];
 #pragma unroll
-                  for (int u = 0; u < 2; ++u) {
+                  for (int u = 0; u < kTiles; ++u) {
                     uint32_t a[4];
                     ldmatrix_x4_trans(vbase + vrow_chunk(t4 + 16 * u + row0, c), a[0], a[1], a[2], a[3]);
 #pragma unroll
@@ -912,12 +945,12 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
                     // a drafted Value that f16 does not hold: zero, so that the nodes that do not see
                     // its token do not get 0 * NaN (those that do get NaN through P)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
+                    for (int i = 0; i < 4 * kTiles; ++i) {
                       if ((f[i] & 0x7C00u) == 0x7C00u) f[i] &= 0xFFFF0000u;
                       if ((f[i] & 0x7C000000u) == 0x7C000000u) f[i] &= 0xFFFFu;
                     }
                   }
-                  tc_st_frag2(tt + ((uint32_t)(16 * e) << 16) + ((part + t4) >> 1), f);
+                  tc_st_frags(tt + ((uint32_t)(16 * e) << 16) + ((part + t4) >> 1), f);
                 }
               }
             }
@@ -939,17 +972,18 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
   } else {
     // ======================= softmax, epilogue =======================
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Sh::kRegSm));
-    const int h = (warp - 8) >> 2;        // column half
+    constexpr int kAllSm = 128 * Sh::kGroups;
+    const int h = (warp - 8) >> 2;        // the warpgroup's columns: kSub h ..
     const int wq = warp & 3;
     const int tok = 32 * wq + lane;       // the thread's tensor-memory lane: token of the scores, channel of the outputs
-    const int th = tid - 256;             // 0 .. 255 over both halves
+    const int th = tid - 256;             // over all groups
     const uint32_t tlane = tm + ((uint32_t)(32 * wq) << 16);
     float* const neg = S.neg + h * SUB;
     const int barid = 1 + h;
     uint32_t g = 0;
     while (tree_next(p, pre, lens, cur, sg)) {
       // ---- the drafted tokens, where this cut reaches a block of theirs ----
-      named_sync(3, 256);  // (the previous cut's epilogue has read S.neg)
+      named_sync(5, kAllSm);  // (the previous cut's epilogue has read S.neg)
       if (th < NT) S.neg[th] = 0.f;
       if (th < 64 && sg.blk1 > sg.nq + (sg.n_sink + sg.r) / kBlk) {
         bool wild = false;
@@ -979,7 +1013,7 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
         uint32_t m = 0;
         const int g16 = th & 7;
 #pragma unroll 1
-        for (int row = th >> 3; row < NT; row += 32) {
+        for (int row = th >> 3; row < NT; row += kAllSm / 8) {
           const int col = sg.ch * NT + row;
           uint4 a = make_uint4(0, 0, 0, 0), b = a;
           if (col < p.gh * p.N) {
@@ -1004,11 +1038,11 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_addr(&S.q_full));
-      named_sync(3, 256);
+      named_sync(5, kAllSm);
       if (th < p.N && sg.blk1 > sg.nq + (sg.n_sink + sg.r) / kBlk) S.anc[th] = tree_ancestors(S.par, th);
-      named_sync(3, 256);
+      named_sync(5, kAllSm);
 
-      constexpr int kCh = SUB == 32 ? 32 : 16;  // columns in registers at a time
+      constexpr int kCh = NT == 64 ? 32 : 16;  // columns in registers at a time
       float l[SUB];
 #pragma unroll
       for (int j = 0; j < SUB; ++j) l[j] = 0.f;
@@ -1063,7 +1097,7 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
             const uint32_t w = (uint32_t)(allow >> c0);
             float x[8];
             tc_ld8(ts + c0, x);
-            tc_wait_ld();
+            tc_wait_ld(x);
 #pragma unroll
             for (int j = 0; j < 8; ++j) x[j] = (w >> j) & 1u ? (spoilt ? NAN : x[j]) : (c > 0.f ? -INFINITY : INFINITY);
             tc_st8(ts + c0, x);
@@ -1073,7 +1107,7 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
         auto load = [&](int c0, float (&x)[kCh]) {
 #pragma unroll
           for (int j = 0; j < kCh; j += 16) tc_ld16(ts + c0 + j, x + j);
-          tc_wait_ld();
+          tc_wait_ld(x);
         };
         // Columns c0 .. of the scores as exponents (log2) relative to the columns' maxima so far, and their largest
         auto exponents = [&](int c0, float (&x)[kCh], float& top) {
@@ -1095,9 +1129,9 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
           }
           top = fmaxf(top, fmaxf(t0, t1));
         };
-        uint8_t* const P = Ps + pb * Sh::kPBytes + (NT == 128 ? h * (kBlk * 128) : 0);
+        uint8_t* const P = Ps + pb * Sh::kPBytes + h * SUB / 64 * (kBlk * 128);
         auto put_p = [&](int col, const float* e) {  // eight columns
-          const uint32_t at = (uint32_t)(tok * Sh::kPRow + (NT == 128 ? 0 : h * SUB * 2) + col * 2);
+          const uint32_t at = (uint32_t)(tok * Sh::kPRow + (h * SUB % 64 + col) * 2);
           *reinterpret_cast<uint4*>(P + (at ^ (((at >> 7) & Sh::kPMask) << 4))) =
               make_uint4(pack_f16(e[0], e[1]), pack_f16(e[2], e[3]), pack_f16(e[4], e[5]), pack_f16(e[6], e[7]));
         };
@@ -1154,7 +1188,7 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
               for (int j0 = 0; j0 < SUB; j0 += 8) {
                 float o[8];
                 tc_ld8(to + j0, o);
-                tc_wait_ld();
+                tc_wait_ld(o);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) o[j] = scaled(o[j], S.fall[h * SUB + j0 + j]);
                 tc_st8(to + j0, o);
@@ -1208,7 +1242,7 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
       }
 
       // ---- epilogue: column sums, then O ----
-      // a lane's sums of all columns -> all lanes' sum of 2 lane, 2 lane + 1 (32 columns: lane; 16: lane / 2):
+      // a lane's sums of all columns -> all lanes' sum of one column (32 columns: lane; 16: lane / 2):
       // each step halves the columns a lane keeps and adds the partner's for those
 #pragma unroll
       for (int w = SUB / 2, bit = 16; bit > 0; w >>= 1, bit >>= 1) {
@@ -1220,12 +1254,7 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
           l[j] = keep + __shfl_xor_sync(kAll, give, bit);
         }
       }
-      if constexpr (SUB == 64) {
-        S.red[wq][h * SUB + 2 * lane] = l[0];
-        S.red[wq][h * SUB + 2 * lane + 1] = l[1];
-      } else if (SUB == 32 || (lane & 1) == 0) {
-        S.red[wq][h * SUB + (SUB == 32 ? lane : lane >> 1)] = l[0];
-      }
+      if (SUB == 32 || (lane & 1) == 0) S.red[wq][h * SUB + (SUB == 32 ? lane : lane >> 1)] = l[0];
       tree_wait(&S.p_free[(g - 1) & 1], ((g - 1) >> 1) & 1, abort, p.status);
       tc_fence_after();
       named_sync(barid, 128);
@@ -1255,7 +1284,7 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
       for (int j0 = 0; j0 < SUB; j0 += 8) {
         float o[8];
         tc_ld8(tlane + Sh::kTmO + h * SUB + j0, o);
-        tc_wait_ld();
+        tc_wait_ld(o);
 #pragma unroll
         for (int jj = 0; jj < 8; ++jj) {
           const int j = h * SUB + j0 + jj, row = S.row[j];
@@ -1268,7 +1297,7 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
       if (!whole) {
         // ---- the last CTA to finish the item merges its parts, in CTA order ----
         __threadfence();
-        named_sync(3, 256);
+        named_sync(5, kAllSm);
         const unsigned U = S.units, W = S.ctas, a0 = sg.item0, a1 = a0 + (unsigned)sg.nblk;
         // the CTAs whose ranges meet [a0, a1)
         unsigned c0 = (unsigned)((unsigned long long)a0 * W / U), c1 = (unsigned)((unsigned long long)(a1 - 1) * W / U);
@@ -1280,13 +1309,13 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
           S.last = n + 1 == c1 - c0 + 1;
           if (S.last) *ctr = 0u;
         }
-        named_sync(3, 256);
+        named_sync(5, kAllSm);
         if (S.last) {
           __threadfence();
           const long long p0 = ((long long)c0 * 2 + (tree_unit(U, W, c0) > a0 ? 0 : 1)) * NT;  // (its first part)
           // a warp per column, four channels a lane
 #pragma unroll 1
-          for (int j = warp - 8; j < NT; j += 8) {
+          for (int j = warp - 8; j < NT; j += Sh::kSmWarps) {
             const int row = S.row[j];
             if (row < 0) continue;
             float m = -INFINITY, sum = 0.f;
@@ -1321,7 +1350,7 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 17) tc_dealloc512(tm);
+  if (warp == Sh::kIo + 1) tc_dealloc512(tm);
 }
 
 template <int FMT, int NT>
