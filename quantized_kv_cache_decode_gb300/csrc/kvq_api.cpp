@@ -857,6 +857,7 @@ kvq_status kvq_decode_attention_tree(const kvq_layer_config* cfg, const kvq_laye
   p.Hq = num_q_heads;
   p.gh = num_q_heads / L.H;
   p.batch = batch;
+  p.most_tokens = (int)std::min<long long>(max_seq_tokens(L), 0x7FFFFFFFLL);
   p.chunks = G.chunks;
   p.nslots = G.nslots;
   p.slot_bytes = G.slot_bytes;

@@ -116,6 +116,7 @@ struct TreeParams {
   const int32_t* parents;  // [B][N]
   const int32_t* seq_lens;
   int N, Hq, gh, batch;
+  int most_tokens;  // that a sequence of the layer can hold (at most INT_MAX)
   int chunks;      // column chunks of NT per (sequence, kv head)
   int nslots, slot_bytes;
   int slot_hdr;    // bytes of a quantized slot before the block's own (integer layers: a record header)
@@ -133,10 +134,10 @@ struct TreeParams {
 
 // CTAs that share a tree launch's blocks: whole items each where all are of one length and fill at
 // least 80 % of the grid that way (nothing is cut and merged), else all CTAs, at least one block each.
-__host__ __device__ inline long long tree_ctas(long long grid, long long blocks, long long items, bool equal) {
+__host__ __device__ inline unsigned tree_ctas(unsigned grid, unsigned blocks, unsigned items, bool equal) {
   if (equal && items > 0) {
-    const long long k = (items + grid - 1) / grid;
-    if (items % k == 0 && (items / k) * 5 >= grid * 4) return items / k;
+    const unsigned k = (items + grid - 1) / grid, n = items / k;
+    if (n * k == items && n * 5 >= grid * 4) return n;
   }
   return blocks < grid ? (blocks < 1 ? 1 : blocks) : grid;
 }

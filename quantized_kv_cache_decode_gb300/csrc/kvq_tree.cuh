@@ -210,6 +210,7 @@ struct TreeCursor {
 };
 
 struct TreeSmem {  // small shared state, after the big buffers
+  // (barriers, in the order that the set-up initialises them in)
   unsigned long long slot_full[kMaxSlots], slot_ready[kMaxSlots], slot_empty[kMaxSlots];
   unsigned long long k_full[2], k_empty[2], v_full[2], v_empty[2];
   unsigned long long s_full[2], s_free[2], p_full[2], p_free[2], q_full, drain;
@@ -279,9 +280,10 @@ struct TileMap {
   __device__ __forceinline__ int record(const TreeParams& p, int j) const { return tile_record(p, t0 + j) - r0; }
 };
 
-// First unit of CTA c of W
+// First unit of CTA c of W: floor(U c / W) without a 64-bit division (U = q W + r, c <= W < 2^16)
 __device__ __forceinline__ unsigned tree_unit(unsigned U, unsigned W, unsigned c) {
-  return (unsigned)((unsigned long long)U * c / W);
+  const unsigned q = U / W, r = U - q * W;
+  return q * c + r * c / W;
 }
 
 // The warp's next cut, in shared memory (roles keep few of its fields in registers); false behind the last.
@@ -291,22 +293,23 @@ __device__ __forceinline__ bool tree_next(const TreeParams& p, const int* pre, c
   if ((threadIdx.x & 31) == 0 && c.u < c.end) {
     const unsigned hc = (unsigned)(p.L.H * p.chunks);
     int b = c.b;
+#pragma unroll 1
     while (b + 1 < p.batch && (unsigned)pre[b + 1] * hc <= c.u) ++b;
     c.b = b;
     const unsigned nblk = (unsigned)(pre[b + 1] - pre[b]);
     const unsigned off = c.u - (unsigned)pre[b] * hc, item = off / nblk, blk0 = off - item * nblk;
     const unsigned left = c.end - c.u, n = left < nblk - blk0 ? left : nblk - blk0;
-    const TokenSplit ts = split_tokens(lens[b], p.L);
+    const int T = lens[b], qn = lens[p.batch + b], n_sink = T < p.L.S ? T : p.L.S;
     s.b = b;
     s.h = (int)(item / (unsigned)p.chunks);
     s.ch = (int)(item % (unsigned)p.chunks);
     s.blk0 = (int)blk0;
     s.blk1 = (int)(blk0 + n);
     s.nblk = (int)nblk;
-    s.nq = (ts.qn + kBlk - 1) / kBlk;
-    s.n_sink = ts.n_sink;
-    s.qn = ts.qn;
-    s.r = ts.r;
+    s.nq = (qn + kBlk - 1) / kBlk;
+    s.n_sink = n_sink;
+    s.qn = qn;
+    s.r = T - n_sink - qn;
     s.item0 = c.u - blk0;
     c.u += n;
   } else if ((threadIdx.x & 31) == 0) {
@@ -435,10 +438,17 @@ __device__ __forceinline__ void load_words(const uint8_t* codes, int lane, int i
 __device__ __forceinline__ float group_reach(float s, float z, float levels) {
   return fabsf(s) * fmaxf(fabsf(z), fabsf(levels - z));
 }
-// whether one of four groups may stand for more than f16 holds (s m + c with |m| <= half)
-__device__ __forceinline__ bool beyond_f16(const float4& s, const float4& c, float half) {
-  return fmaxf(fmaxf(fmaf(fabsf(s.x), half, fabsf(c.x)), fmaf(fabsf(s.y), half, fabsf(c.y))),
-               fmaxf(fmaf(fabsf(s.z), half, fabsf(c.z)), fmaf(fabsf(s.w), half, fabsf(c.w)))) >= 65000.f;
+// four groups' scales and zero points as f16 pairs {s01, s23, c01, c23} with c = s (half - z); `worst` gets the largest
+// magnitude that they stand for where that may be more than f16 holds (s m + c with |m| <= half) and `used`
+__device__ __forceinline__ uint4 f16_scales(const float4& s, const float4& z, float half, float levels, bool used,
+                                            float& worst) {
+  const float4 c = make_float4(s.x * (half - z.x), s.y * (half - z.y), s.z * (half - z.z), s.w * (half - z.w));
+  const float most = fmaxf(fmaxf(fmaf(fabsf(s.x), half, fabsf(c.x)), fmaf(fabsf(s.y), half, fabsf(c.y))),
+                           fmaxf(fmaf(fabsf(s.z), half, fabsf(c.z)), fmaf(fabsf(s.w), half, fabsf(c.w))));
+  if (__builtin_expect(most >= 65000.f && used, 0))
+    worst = fmaxf(worst, fmaxf(fmaxf(group_reach(s.x, z.x, levels), group_reach(s.y, z.y, levels)),
+                               fmaxf(group_reach(s.z, z.z, levels), group_reach(s.w, z.w, levels))));
+  return make_uint4(pack_f16(s.x, s.y), pack_f16(s.z, s.w), pack_f16(c.x, c.y), pack_f16(c.z, c.w));
 }
 // f16 pair of tokens t, t + 1: all ones where the token is below n
 __device__ __forceinline__ uint32_t pair_mask(int t, int n) {
@@ -485,30 +495,24 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
   TreeSmem& S = *reinterpret_cast<TreeSmem*>(slots + (size_t)p.nslots * p.slot_bytes);
   int* const pre = reinterpret_cast<int*>(&S + 1);  // [batch + 1] blocks before
   int* const lens = pre + p.batch + 1;              // [batch] tokens
+  int* const quants = lens + p.batch;               // [batch] those in the quantized store
 
   // ---- set-up: barriers, tensor memory, the batch's block counts ----
-  if (tid == 0) {
-    for (int i = 0; i < kMaxSlots; ++i) {
-      mbar_init(smem_addr(&S.slot_full[i]), 32);
-      mbar_init(smem_addr(&S.slot_ready[i]), 1);
-      mbar_init(smem_addr(&S.slot_empty[i]), 8);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_addr(&S.k_full[i]), 4);
-      mbar_init(smem_addr(&S.k_empty[i]), 1);
-      mbar_init(smem_addr(&S.v_full[i]), 4);
-      mbar_init(smem_addr(&S.v_empty[i]), 1);
-      mbar_init(smem_addr(&S.s_full[i]), 1);
-      mbar_init(smem_addr(&S.s_free[i]), Sh::kSmWarps);
-      mbar_init(smem_addr(&S.p_full[i]), Sh::kSmWarps);
-      mbar_init(smem_addr(&S.p_free[i]), 1);
-    }
-    mbar_init(smem_addr(&S.q_full), Sh::kSmWarps);
-    mbar_init(smem_addr(&S.drain), 1);
+  // (a thread per barrier and 32-bit divisions below: this code runs once, and every instruction of it is fetched
+  // from beyond the SM, so a small call costs what its length costs)
+  if (tid < 3 * kMaxSlots) {
+    const int kind = tid / kMaxSlots;  // slot_full, slot_ready, slot_empty
+    mbar_init(smem_addr(S.slot_full + tid), kind == 0 ? 32 : (kind == 1 ? 1 : 8));
+  } else if (tid < 3 * kMaxSlots + 18) {
+    const int i = tid - 3 * kMaxSlots;  // k_full k_empty v_full v_empty s_full s_free p_full p_free (two each) q_full drain
+    const int kind = i >> 1;
+    mbar_init(smem_addr(S.k_full + i), kind == 0 || kind == 2 ? 4 : (kind == 5 || kind == 6 || i == 16 ? Sh::kSmWarps : 1));
+  } else if (tid < 3 * kMaxSlots + 22) {
+    S.unset[tid - 3 * kMaxSlots - 18] = 0;
+  } else if (tid == 3 * kMaxSlots + 22) {
     S.abort = 0;
-    for (int i = 0; i < 4; ++i) S.unset[i] = 0;
-    fence_barrier_init();
   }
+  if (tid < 64) fence_barrier_init();
   if (warp == Sh::kIo + 1) {
     tc_alloc512(smem_addr(&S.tmem));
     tc_relinquish();
@@ -519,16 +523,16 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
     S.kscale = F::kFp8 ? *p.C.k_tscale : 1.f;
     S.vunit = F::kFp8 ? *p.C.v_tscale * (FMT == KVQ_FMT_FP8_E5M2 ? 256.f : 1.f) : 1.f;
   }
+#pragma unroll 1
   for (int b = tid; b < p.batch; b += Sh::kThreads) {
-    long long T = p.seq_lens[b];
-    const long long cap = max_tokens(L);
-    if (T > cap) {
+    int T = p.seq_lens[b];
+    if (T > p.most_tokens) {
       if (blockIdx.x == 0) report(p.status, KVQ_DEV_CAPACITY);
-      T = cap;
+      T = p.most_tokens;
     }
-    if (T < 0) T = 0;
-    const TokenSplit ts = split_tokens((int)T, L);
-    lens[b] = (int)T;
+    const TokenSplit ts = split_tokens(T < 0 ? 0 : T, L);
+    lens[b] = ts.n_sink + ts.qn + ts.r;
+    quants[b] = ts.qn;
     pre[b + 1] = (ts.qn + kBlk - 1) / kBlk + (ts.n_sink + ts.r + p.N + kBlk - 1) / kBlk;
   }
   __syncthreads();
@@ -559,7 +563,8 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
   TreeCursor& cur = S.cur[warp];
   TreeSeg& sg = S.seg[warp];
   if (lane == 0) {
-    const unsigned U = (unsigned)pre[p.batch] * (unsigned)(L.H * p.chunks), W = (unsigned)tree_ctas(gridDim.x, U, (long long)p.batch * L.H * p.chunks, S.least == S.most);
+    const unsigned U = (unsigned)pre[p.batch] * (unsigned)(L.H * p.chunks),
+                   W = tree_ctas(gridDim.x, U, (unsigned)(p.batch * L.H * p.chunks), S.least == S.most);
     S.units = U;
     S.ctas = W;
     const unsigned c = blockIdx.x;
@@ -628,8 +633,8 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
               if (!(ok = tree_wait(&S.slot_empty[slot], ph, abort, p.status))) break;
               uint8_t* const dst = slots + (size_t)slot * p.slot_bytes;
               const int c = lane & 15;
-              int at = x0 + part - n_sink;  // ring slot of the first row (rows before it do not use it)
-              at = (int)(((long long)qn + (at < 0 ? 0 : at)) % (L.W > 0 ? L.W : 1));
+              const int back = x0 + part - n_sink;  // ring slot of the first row (rows before it do not use it)
+              int at = (int)((unsigned)(qn + (back < 0 ? 0 : back)) % (unsigned)(L.W > 0 ? L.W : 1));
 #pragma unroll 4
               for (int i = 0; i < p.bf_tokens; ++i) {
                 const int x = x0 + part + i;
@@ -745,38 +750,47 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
                   S.tile_at[slot][lane] = map.tile(p, lane, e);
                   S.head_at[slot][lane] = map.header(p, e);
                 }
+                __syncwarp();
+                // two at a time: both read, then both written over
 #pragma unroll 1
-                for (int e = 0; e < nh; ++e) {  // (a header whose tiles were not copied holds anything, and is not used)
-                  uint8_t* const hdr = src + map.header(p, e);
-                  const float4 sc = reinterpret_cast<const float4*>(hdr)[lane];
-                  const float4 z = reinterpret_cast<const float4*>(hdr + 512)[lane];
-                  const float4 c = make_float4(sc.x * (kHalf - z.x), sc.y * (kHalf - z.y), sc.z * (kHalf - z.z), sc.w * (kHalf - z.w));
-                  const int ti = e == 0 ? 0 : (map.r0 + e) * L.tpg - map.t0;  // its first tile of the block
-                  if (beyond_f16(sc, c, kHalf) && ((okmask >> ti) & 1u))
-                    worst = fmaxf(worst, fmaxf(fmaxf(group_reach(sc.x, z.x, kL), group_reach(sc.y, z.y, kL)),
-                                               fmaxf(group_reach(sc.z, z.z, kL), group_reach(sc.w, z.w, kL))));
+                for (int e0 = 0; e0 < nh; e0 += 2) {  // (a header whose tiles were not copied holds anything, and is not used)
+                  uint8_t* hdr[2];
+                  uint4 out[2];
+#pragma unroll
+                  for (int k = 0; k < 2; ++k) {
+                    const int e = min(e0 + k, nh - 1);
+                    hdr[k] = src + map.header(p, e);
+                    const float4 sc = reinterpret_cast<const float4*>(hdr[k])[lane];
+                    const float4 z = reinterpret_cast<const float4*>(hdr[k] + 512)[lane];
+                    const int ti = e == 0 ? 0 : (map.r0 + e) * L.tpg - map.t0;  // its first tile of the block
+                    out[k] = f16_scales(sc, z, kHalf, kL, (okmask >> ti) & 1u, worst);
+                  }
                   __syncwarp();
-                  reinterpret_cast<uint4*>(hdr)[lane] =
-                      make_uint4(pack_f16(sc.x, sc.y), pack_f16(sc.z, sc.w), pack_f16(c.x, c.y), pack_f16(c.z, c.w));
+#pragma unroll
+                  for (int k = 0; k < 2; ++k) reinterpret_cast<uint4*>(hdr[k])[lane] = out[k];
                 }
                 // Values: a lane per (tile, q, group), the tokens 2q, 2q + 1, 2q + 8, 2q + 9; whole tiles at a time
 #pragma unroll 1
-                for (int at = lane; at < 32 * ngv; at += 32) {
-                  const int ti = at >> (2 + lg), within = at & (4 * ngv - 1), vq = within >> lg, j = within & (ngv - 1);
-                  uint8_t* const to = src + map.tile(p, ti, map.record(p, ti)) + 32 * F::kRb;
-                  const float* const f = reinterpret_cast<const float*>(to) + 2 * vq * ngv + j;
-                  uint4 out = make_uint4(0u, 0u, 0u, 0u);  // (a tile that was not copied: all its Values zero)
-                  if ((okmask >> ti) & 1u) {
-                    const float4 sc = make_float4(f[0], f[ngv], f[8 * ngv], f[9 * ngv]);
-                    const float4 z = make_float4(f[16 * ngv], f[17 * ngv], f[24 * ngv], f[25 * ngv]);
-                    const float4 c = make_float4(sc.x * (kHalf - z.x), sc.y * (kHalf - z.y), sc.z * (kHalf - z.z), sc.w * (kHalf - z.w));
-                    if (beyond_f16(sc, c, kHalf))
-                      worst = fmaxf(worst, fmaxf(fmaxf(group_reach(sc.x, z.x, kL), group_reach(sc.y, z.y, kL)),
-                                                 fmaxf(group_reach(sc.z, z.z, kL), group_reach(sc.w, z.w, kL))));
-                    out = make_uint4(pack_f16(sc.x, sc.y), pack_f16(sc.z, sc.w), pack_f16(c.x, c.y), pack_f16(c.z, c.w));
+                for (int at0 = lane; at0 < 32 * ngv; at0 += 64) {
+                  uint8_t* to[2];
+                  uint4 out[2];
+#pragma unroll
+                  for (int k = 0; k < 2; ++k) {
+                    const int at = ngv == 1 ? at0 : at0 + 32 * k;
+                    const int ti = at >> (2 + lg), within = at & (4 * ngv - 1), vq = within >> lg, j = within & (ngv - 1);
+                    uint8_t* const base = src + S.tile_at[slot][ti] + 32 * F::kRb;
+                    const float* const f = reinterpret_cast<const float*>(base) + 2 * vq * ngv + j;
+                    to[k] = base + j * 64 + vq * 16;
+                    out[k] = make_uint4(0u, 0u, 0u, 0u);  // (a tile that was not copied: all its Values zero)
+                    if ((okmask >> ti) & 1u) {
+                      const float4 sc = make_float4(f[0], f[ngv], f[8 * ngv], f[9 * ngv]);
+                      const float4 z = make_float4(f[16 * ngv], f[17 * ngv], f[24 * ngv], f[25 * ngv]);
+                      out[k] = f16_scales(sc, z, kHalf, kL, true, worst);
+                    }
                   }
                   __syncwarp();
-                  *reinterpret_cast<uint4*>(to + j * 64 + vq * 16) = out;
+#pragma unroll
+                  for (int k = 0; k < 2; ++k) *reinterpret_cast<uint4*>(to[k]) = out[k];
                 }
               }
               // (these writes come before the slot's next bulk copy)
@@ -1300,7 +1314,8 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
         named_sync(5, kAllSm);
         const unsigned U = S.units, W = S.ctas, a0 = sg.item0, a1 = a0 + (unsigned)sg.nblk;
         // the CTAs whose ranges meet [a0, a1)
-        unsigned c0 = (unsigned)((unsigned long long)a0 * W / U), c1 = (unsigned)((unsigned long long)(a1 - 1) * W / U);
+        const unsigned most = U / W + 1;  // units of a CTA, at most
+        unsigned c0 = a0 / most, c1 = (a1 - 1) / most;
         while (tree_unit(U, W, c0 + 1) <= a0) ++c0;
         while (tree_unit(U, W, c1 + 1) <= a1 - 1) ++c1;
         if (th == 0) {
@@ -1320,7 +1335,7 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
             if (row < 0) continue;
             float m = -INFINITY, sum = 0.f;
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+#pragma unroll 2
             for (unsigned cc = c0; cc <= c1; ++cc) {
               const long long at = (cc == c0 ? p0 : (long long)cc * 2 * NT) + j;
               const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.ws_ml) + at);
