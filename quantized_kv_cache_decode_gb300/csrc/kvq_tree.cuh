@@ -176,7 +176,7 @@ struct TreeShape {
   static constexpr int kWarps = kIo + 4, kThreads = 32 * kWarps;
   // registers a thread: at launch, then by role (the roles' warpgroups together stay within the launch's)
   static constexpr int kRegLaunch = NT == 128 ? 72 : 96;
-  static constexpr int kRegDq = NT == 128 ? 56 : 80, kRegSm = NT == 128 ? 88 : 128, kRegIo = NT == 128 ? 40 : 64;
+  static constexpr int kRegDq = NT == 128 ? 48 : 80, kRegSm = NT == 128 ? 88 : 128, kRegIo = NT == 128 ? 56 : 64;
   static_assert(2 * kRegDq + kGroups * kRegSm + kRegIo <= (kWarps / 4) * kRegLaunch, "register split");
   static constexpr int kQBytes = NT * 256;         // queries (f16): [two 64-channel halves][NT rows of 128 bytes]
   static constexpr int kPBytes = kBlk * NT * 2;    // one buffer of P (f16)
@@ -631,24 +631,34 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
             const int nsr = n_sink + sg.r, nrow = nsr + p.N;
             for (int part = 0; part < kBlk; part += p.bf_tokens) {
               if (!(ok = tree_wait(&S.slot_empty[slot], ph, abort, p.status))) break;
-              uint8_t* const dst = slots + (size_t)slot * p.slot_bytes;
+              const uint32_t dst = smem_addr(slots + (size_t)slot * p.slot_bytes) + (kv ? p.bf_tokens * 256 : 0);
               const int c = lane & 15;
-              const int back = x0 + part - n_sink;  // ring slot of the first row (rows before it do not use it)
-              int at = (int)((unsigned)(qn + (back < 0 ? 0 : back)) % (unsigned)(L.W > 0 ? L.W : 1));
-#pragma unroll 4
-              for (int i = 0; i < p.bf_tokens; ++i) {
+              // runs of rows that follow one another in memory: sink, ring up to its end, ring, drafts; then zeros
+              for (int i = 0; i < p.bf_tokens;) {
                 const int x = x0 + part + i;
                 const __nv_bfloat16* src = draft;
-                uint32_t n = 16;
-                if (x < n_sink) src = sink + (pair * L.S + x) * L.d;
-                else if (x < nsr) {
+                int n = p.bf_tokens - i;
+                uint32_t size = 16;
+                if (x < n_sink) {
+                  src = sink + (pair * L.S + x) * L.d;
+                  n = min(n, n_sink - x);
+                } else if (x < nsr) {
+                  const int at = (int)((unsigned)(qn + (x - n_sink)) % (unsigned)L.W);
                   src = ring + (pair * L.W + at) * L.d;
-                  if (++at == L.W) at = 0;
-                } else if (x < nrow) src = draft + (pair * p.N + (x - nsr)) * L.d;
-                else n = 0;  // rows behind the list: zeros
-                const uint32_t to = smem_addr(dst) + (kv ? p.bf_tokens * 256 + vrow_chunk(i, c) : krow_chunk(i, c));
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(src + c * 8), "r"(n)
-                             : "memory");
+                  n = min(n, min(nsr - x, L.W - at));
+                } else if (x < nrow) {
+                  src = draft + (pair * p.N + (x - nsr)) * L.d;
+                  n = min(n, nrow - x);
+                } else {
+                  size = 0;  // rows behind the list
+                }
+                src += c * 8;
+                const int step = size ? L.d : 0;
+#pragma unroll 8
+                for (const int end = i + n; i < end; ++i, src += step) {
+                  const uint32_t to = dst + (kv ? vrow_chunk(i, c) : krow_chunk(i, c));
+                  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(src), "r"(size));
+                }
               }
               asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
                                smem_addr(&S.slot_full[slot]))
