@@ -176,7 +176,7 @@ struct TreeShape {
   static constexpr int kWarps = kIo + 4, kThreads = 32 * kWarps;
   // registers a thread: at launch, then by role (the roles' warpgroups together stay within the launch's)
   static constexpr int kRegLaunch = NT == 128 ? 72 : 96;
-  static constexpr int kRegDq = NT == 128 ? 48 : 80, kRegSm = NT == 128 ? 88 : 128, kRegIo = NT == 128 ? 56 : 64;
+  static constexpr int kRegDq = NT == 128 ? 56 : 80, kRegSm = NT == 128 ? 88 : 128, kRegIo = NT == 128 ? 40 : 64;
   static_assert(2 * kRegDq + kGroups * kRegSm + kRegIo <= (kWarps / 4) * kRegLaunch, "register split");
   static constexpr int kQBytes = NT * 256;         // queries (f16): [two 64-channel halves][NT rows of 128 bytes]
   static constexpr int kPBytes = kBlk * NT * 2;    // one buffer of P (f16)
@@ -741,6 +741,7 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
       bool ok = true;
       float worst = 0.f;  // largest magnitude that any group stands for
       const int ngv = L.ngv, lg = 31 - __clz(ngv);
+      constexpr int kTwo = NT == 128 ? 1 : 2;  // (registers)
       while (ok && tree_next(p, pre, lens, cur, sg)) {
         const int blk1 = sg.blk1, nq = sg.nq;
         for (int blk = sg.blk0; ok && blk < blk1; ++blk) {
@@ -761,13 +762,13 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
                   S.head_at[slot][lane] = map.header(p, e);
                 }
                 __syncwarp();
-                // two at a time: both read, then both written over
+                // kTwo at a time: all read, then all written over
 #pragma unroll 1
-                for (int e0 = 0; e0 < nh; e0 += 2) {  // (a header whose tiles were not copied holds anything, and is not used)
-                  uint8_t* hdr[2];
-                  uint4 out[2];
+                for (int e0 = 0; e0 < nh; e0 += kTwo) {  // (a header whose tiles were not copied holds anything, and is not used)
+                  uint8_t* hdr[kTwo];
+                  uint4 out[kTwo];
 #pragma unroll
-                  for (int k = 0; k < 2; ++k) {
+                  for (int k = 0; k < kTwo; ++k) {
                     const int e = min(e0 + k, nh - 1);
                     hdr[k] = src + map.header(p, e);
                     const float4 sc = reinterpret_cast<const float4*>(hdr[k])[lane];
@@ -777,15 +778,15 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
                   }
                   __syncwarp();
 #pragma unroll
-                  for (int k = 0; k < 2; ++k) reinterpret_cast<uint4*>(hdr[k])[lane] = out[k];
+                  for (int k = 0; k < kTwo; ++k) reinterpret_cast<uint4*>(hdr[k])[lane] = out[k];
                 }
                 // Values: a lane per (tile, q, group), the tokens 2q, 2q + 1, 2q + 8, 2q + 9; whole tiles at a time
 #pragma unroll 1
-                for (int at0 = lane; at0 < 32 * ngv; at0 += 64) {
-                  uint8_t* to[2];
-                  uint4 out[2];
+                for (int at0 = lane; at0 < 32 * ngv; at0 += 32 * kTwo) {
+                  uint8_t* to[kTwo];
+                  uint4 out[kTwo];
 #pragma unroll
-                  for (int k = 0; k < 2; ++k) {
+                  for (int k = 0; k < kTwo; ++k) {
                     const int at = ngv == 1 ? at0 : at0 + 32 * k;
                     const int ti = at >> (2 + lg), within = at & (4 * ngv - 1), vq = within >> lg, j = within & (ngv - 1);
                     uint8_t* const base = src + S.tile_at[slot][ti] + 32 * F::kRb;
@@ -800,7 +801,7 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
                   }
                   __syncwarp();
 #pragma unroll
-                  for (int k = 0; k < 2; ++k) *reinterpret_cast<uint4*>(to[k]) = out[k];
+                  for (int k = 0; k < kTwo; ++k) *reinterpret_cast<uint4*>(to[k]) = out[k];
                 }
               }
               // (these writes come before the slot's next bulk copy)
