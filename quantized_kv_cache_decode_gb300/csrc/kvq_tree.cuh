@@ -734,10 +734,10 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
       }
       __syncwarp();
     } else if (!F::kFp8) {
-      // ======================= prep: scales to f16, two warps in turn =======================
+      // ======================= prep: scales to f16, two warps, the even and the odd slots =======================
       constexpr float kL = (float)((1 << F::kBits) - 1), kHalf = (float)(1 << (F::kBits - 1));
       int slot = 0;
-      uint32_t ph = 0, n = 0;
+      uint32_t ph = 0;
       bool ok = true;
       float worst = 0.f;  // largest magnitude that any group stands for
       const int ngv = L.ngv, lg = 31 - __clz(ngv);
@@ -747,8 +747,10 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
         for (int blk = sg.blk0; ok && blk < blk1; ++blk) {
           const bool quant = blk < nq;
           const int parts = quant ? 1 : kBlk / p.bf_tokens;
-          for (int i = 0; i < parts; ++i, ++n) {
-            if ((n & 1) == (uint32_t)(warp & 1)) {
+          for (int i = 0; i < parts; ++i) {
+            // A warp owns slots, not turns: having seen every phase of a slot's barrier it cannot take an older
+            // phase of the same parity for the one it waits for.
+            if (((slot ^ warp) & 1) == 0) {
               if (!(ok = tree_wait(&S.slot_full[slot], ph, abort, p.status))) break;
               if (quant) {
                 const uint32_t okmask = S.slot_ok[slot];
