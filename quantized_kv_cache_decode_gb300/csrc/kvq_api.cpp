@@ -792,6 +792,7 @@ kvq_status tree_geometry(const LayerDesc& L, int batch, int columns, TreeGeom* G
   const size_t budget = 227 * 1024;
   if (fixed + 2 * (size_t)G->slot_bytes > budget) return KVQ_ERR_UNSUPPORTED;
   G->nslots = (int)std::min<size_t>(12, (budget - fixed) / G->slot_bytes);
+  if (headers && G->nslots > 4) G->nslots &= ~1;  // (two prep warps share the slots evenly)
   G->smem = (int)(fixed + (size_t)G->nslots * G->slot_bytes);
   const size_t rows = 2 * (size_t)G->ctas * G->nt;
   G->off_ml = rows * kHeadDim * sizeof(float);

@@ -54,59 +54,70 @@ __global__ void __launch_bounds__(32 * kRopeWarps) norm_rope_kernel(const __grid
       sincospif((float)top * 4.656612873077393e-10f, &sn[i], &cs[i]);
     }
   }
-  float wq[16], wk[16];
   const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.qkv) + row * p.row_stride);
+  const long long base = (b * p.H) * p.n_tokens + t;  // row of kv head 0 in k_out and v_out
+  uint4 a = make_uint4(0, 0, 0, 0), c = a;
+  auto load = [&](int g) {  // head h0 + 4 g + sub
+    const int h = h0 + 4 * g + sub;
+    if (g < per && h < heads) {
+      a = __ldcs(src + h * 16 + j);
+      c = __ldcs(src + h * 16 + 8 + j);
+    }
+  };
+  load(0);
+#pragma unroll 2
   for (int g = 0; g < per; ++g) {
     const int h = h0 + 4 * g + sub;
-    const bool on = h < heads;
-    uint4 a = make_uint4(0, 0, 0, 0), c = a;
-    if (on) {
-      a = src[h * 16 + j];
-      c = src[h * 16 + 8 + j];
-    }
+    const uint4 a0 = a, c0 = c;
+    load(g + 1);  // the next heads on their way
+    if (__all_sync(0xffffffffu, h >= heads)) break;
     const bool isq = h < p.Hq, isk = !isq && h < p.Hq + p.H;
-    const uint4* w = reinterpret_cast<const uint4*>(isq ? p.q_weight : p.k_weight);
-    float x[8], y[8];
-    bf16x8_to_f32(a, x);
-    bf16x8_to_f32(c, y);
-    float ss = 0.f;
+    uint4 lo = a0, hi = c0;
+    if (__any_sync(0xffffffffu, isq || isk)) {
+      const uint4* w = reinterpret_cast<const uint4*>(isq ? p.q_weight : p.k_weight);
+      float x[8], y[8];
+      bf16x8_to_f32(a0, x);
+      bf16x8_to_f32(c0, y);
+      float ss = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], fmaf(y[i], y[i], ss));
+      for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], fmaf(y[i], y[i], ss));
 #pragma unroll
-    for (int o = 1; o < 8; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    if (!on) continue;
-    if (isq || isk) {
-      if (w) {
-        const float r = 1.0f / sqrtf(ss * (1.0f / 128.0f) + p.eps);
-        float u[8], v[8];
-        bf16x8_to_f32(w[j], u);
-        bf16x8_to_f32(w[8 + j], v);
+      for (int o = 1; o < 8; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      if (isq || isk) {
+        if (w) {
+          const float r = 1.0f / sqrtf(ss * (1.0f / 128.0f) + p.eps);
+          float u[8], v[8];
+          bf16x8_to_f32(__ldg(w + j), u);
+          bf16x8_to_f32(__ldg(w + 8 + j), v);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          x[i] = x[i] * r * u[i];
-          y[i] = y[i] * r * v[i];
+          for (int i = 0; i < 8; ++i) {
+            x[i] = x[i] * r * u[i];
+            y[i] = y[i] * r * v[i];
+          }
         }
-      }
-      if (p.rotate && h < rotated) {
+        if (p.rotate && h < rotated) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float xi = x[i];
-          x[i] = xi * cs[i] - y[i] * sn[i];
-          y[i] = y[i] * cs[i] + xi * sn[i];
+          for (int i = 0; i < 8; ++i) {
+            const float xi = x[i];
+            x[i] = xi * cs[i] - y[i] * sn[i];
+            y[i] = y[i] * cs[i] + xi * sn[i];
+          }
         }
+        lo = f32_to_bf16x8(x);
+        hi = f32_to_bf16x8(y);
       }
-      a = f32_to_bf16x8(x);
-      c = f32_to_bf16x8(y);
     }
-    uint4* dst;
-    if (isq) {
-      dst = reinterpret_cast<uint4*>(p.q_out) + (row * p.Hq + h) * 16;
-    } else {
-      const int hk = isk ? h - p.Hq : h - p.Hq - p.H;
-      dst = reinterpret_cast<uint4*>(isk ? p.k_out : p.v_out) + ((b * p.H + hk) * p.n_tokens + t) * 16;
+    if (h < heads) {
+      uint4* dst;
+      if (isq) {
+        dst = reinterpret_cast<uint4*>(p.q_out) + (row * p.Hq + h) * 16;
+      } else {
+        const int hk = isk ? h - p.Hq : h - p.Hq - p.H;
+        dst = reinterpret_cast<uint4*>(isk ? p.k_out : p.v_out) + (base + (long long)hk * p.n_tokens) * 16;
+      }
+      dst[j] = lo;
+      dst[8 + j] = hi;
     }
-    dst[j] = a;
-    dst[8 + j] = c;
   }
 }
 
