@@ -320,12 +320,20 @@ __device__ __forceinline__ bool tree_next(const TreeParams& p, const int* pre, c
 }
 
 // Wait for a barrier phase; false when the bound ran out here or elsewhere in the CTA.
+__device__ __forceinline__ bool tree_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+               : "=r"(ok)
+               : "r"(bar), "r"(parity)
+               : "memory");
+  return ok != 0;
+}
 __device__ __forceinline__ bool tree_wait(unsigned long long* bar, uint32_t parity, volatile int* abort,
                                           uint32_t* status) {
   const uint32_t a = smem_addr(bar);
-  if (__builtin_expect(mbar_try_wait(a, parity), 1)) return true;
+  if (__builtin_expect(tree_try(a, parity), 1)) return true;
   const long long t0 = clock64();
-  while (!mbar_try_wait(a, parity)) {
+  while (!tree_try(a, parity)) {
     if (__builtin_expect(*abort != 0, 0)) return false;
     if (__builtin_expect(clock64() - t0 > kTreeWait, 0)) {
       *abort = 1;
