@@ -482,7 +482,8 @@ kvq_status kvq_qk_norm_rope(const void* qkv, int64_t row_stride, int32_t batch, 
  *   k_draft, v_draft  device bf16 [batch][H][n_nodes][d], 16-byte aligned: the
  *             nodes' own keys and values, read from here (they are not in the cache)
  *   seq_lens  device int32 [batch]: tokens in the cache (the tree not among them)
- *   out       device [batch][n_nodes][num_q_heads][d] (fp32 or bf16 as above)
+ *   out       device [batch][n_nodes][num_q_heads][d] (fp32 or bf16 as above), 16-byte
+ *             aligned
  *   lse       device f32 [batch][n_nodes][num_q_heads] or NULL
  *   workspace at least kvq_decode_workspace_size_tree() bytes, 16-byte aligned,
  *             zero-filled once before first use (arrival counters, as for

@@ -840,7 +840,8 @@ kvq_status kvq_decode_attention_tree(const kvq_layer_config* cfg, const kvq_laye
   if ((st = check_cache(L, cache)) != KVQ_OK) return st;
   if (batch == 0) return KVQ_OK;
   if (!q || !k_draft || !v_draft || !parents || !seq_lens || !out || !workspace || !aligned16(q) ||
-      !aligned16(k_draft) || !aligned16(v_draft) || !aligned16(workspace) || !(softmax_scale == softmax_scale))
+      !aligned16(k_draft) || !aligned16(v_draft) || !aligned16(out) || !aligned16(workspace) ||
+      !(softmax_scale == softmax_scale))
     return KVQ_ERR_INVALID_ARG;
   TreeGeom G;
   if ((st = tree_geometry(L, batch, num_q_heads / L.H * n_nodes, &G)) != KVQ_OK) return st;

@@ -1349,35 +1349,65 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
         if (S.last) {
           __threadfence();
           const long long p0 = ((long long)c0 * 2 + (tree_unit(U, W, c0) > a0 ? 0 : 1)) * NT;  // (its first part)
-          // a warp per column, four channels a lane
-#pragma unroll 1
-          for (int j = warp - 8; j < NT; j += Sh::kSmWarps) {
-            const int row = S.row[j];
-            if (row < 0) continue;
+          // each column's maximum and sum over the parts
+          if (th < NT && S.row[th] >= 0) {
             float m = -INFINITY, sum = 0.f;
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+            for (unsigned cc = c0; cc <= c1; ++cc)
+              m = fmaxf(m, __ldcg(p.ws_ml + ((cc == c0 ? p0 : (long long)cc * 2 * NT) + th) * 2));
+            if (m != -INFINITY) {
+#pragma unroll 2
+              for (unsigned cc = c0; cc <= c1; ++cc) {
+                const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.ws_ml) + (cc == c0 ? p0 : (long long)cc * 2 * NT) + th);
+                sum += ml.y * exp2_approx(ml.x - m);
+              }
+            }
+            S.neg[th] = m == -INFINITY ? 0.f : -m;
+            S.fall[th] = sum == 0.f ? 0.f : vunit / sum;
+            if (p.lse) p.lse[S.row[th]] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.69314718055994531f;
+          }
+          named_sync(5, kAllSm);
+          // a warp per four columns, four channels a lane: their loads are in flight together
+#pragma unroll 1
+          for (int j = (warp - 8) * 4; j < NT; j += Sh::kSmWarps * 4) {
+            float4 acc[4];
+            float neg4[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+              neg4[k] = S.neg[j + k];
+            }
 #pragma unroll 2
             for (unsigned cc = c0; cc <= c1; ++cc) {
               const long long at = (cc == c0 ? p0 : (long long)cc * 2 * NT) + j;
-              const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.ws_ml) + at);
-              const float4 o = __ldcg(reinterpret_cast<const float4*>(p.ws_o + at * L.d) + lane);
-              if (ml.x == -INFINITY) continue;
-              const float mn = fmaxf(m, ml.x);
-              const float fa = m == -INFINITY ? 0.f : exp2_approx(m - mn), fb = exp2_approx(ml.x - mn);
-              sum = sum * fa + ml.y * fb;
-              acc.x = acc.x * fa + o.x * fb;
-              acc.y = acc.y * fa + o.y * fb;
-              acc.z = acc.z * fa + o.z * fb;
-              acc.w = acc.w * fa + o.w * fb;
-              m = mn;
+              float4 o[4];
+              float w[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {  // (columns behind the last one: what lies there is not used)
+                w[k] = __ldcg(p.ws_ml + (at + k) * 2);
+                o[k] = __ldcg(reinterpret_cast<const float4*>(p.ws_o + (at + k) * L.d) + lane);
+              }
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const float f = exp2_approx(w[k] + neg4[k]);
+                if (w[k] == -INFINITY) continue;  // (no token of that part)
+                acc[k].x = fmaf(o[k].x, f, acc[k].x);
+                acc[k].y = fmaf(o[k].y, f, acc[k].y);
+                acc[k].z = fmaf(o[k].z, f, acc[k].z);
+                acc[k].w = fmaf(o[k].w, f, acc[k].w);
+              }
             }
-            const float inv = sum == 0.f ? 0.f : vunit / sum;
-            put_out(p, row, 4 * lane, inv == 0.f ? 0.f : acc.x * inv);
-            put_out(p, row, 4 * lane + 1, inv == 0.f ? 0.f : acc.y * inv);
-            put_out(p, row, 4 * lane + 2, inv == 0.f ? 0.f : acc.z * inv);
-            put_out(p, row, 4 * lane + 3, inv == 0.f ? 0.f : acc.w * inv);
-            if (p.lse && lane == 0)
-              p.lse[row] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.69314718055994531f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int row = S.row[j + k];
+              const float inv = S.fall[j + k];
+              if (row < 0) continue;
+              const float4 v = inv == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
+                                          : make_float4(acc[k].x * inv, acc[k].y * inv, acc[k].z * inv, acc[k].w * inv);
+              const long long to = (long long)row * 32 + lane;  // in units of four channels
+              if (p.out_bf16) reinterpret_cast<uint2*>(p.out)[to] = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+              else reinterpret_cast<float4*>(p.out)[to] = v;
+            }
           }
         }
       }

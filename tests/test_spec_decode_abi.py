@@ -68,7 +68,7 @@ def layer(kvq, fmt="int4", **kw):
 @pytest.mark.parametrize("bad,status", [
     (dict(n_nodes=0), -1), (dict(n_nodes=65), -1), (dict(batch=-1), -1), (dict(batch=2049), -1),
     (dict(num_q_heads=3), -1), (dict(num_q_heads=18), -1), (dict(out_bf16=2), -1), (dict(q=8), -1), (dict(q=0), -1),
-    (dict(k_draft=0), -1), (dict(v_draft=24), -1), (dict(parents=0), -1), (dict(seq_lens=0), -1), (dict(out=0), -1),
+    (dict(k_draft=0), -1), (dict(v_draft=24), -1), (dict(parents=0), -1), (dict(seq_lens=0), -1), (dict(out=0), -1), (dict(out=4104), -1),
     (dict(softmax_scale=float("nan")), -1), (dict(workspace=0), -1), (dict(workspace=8), -1)])
 def test_decode_attention_tree_refusals(kvq, bad, status):
     cfg, cache = layer(kvq)
