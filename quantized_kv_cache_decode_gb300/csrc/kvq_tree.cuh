@@ -193,6 +193,9 @@ struct TreeShape {
   static constexpr uint32_t kPSwizzle = NT == 32 ? 4 : 2, kPMask = NT == 32 ? 3 : 7;
 };
 
+// Items of at most so many blocks are not cut where every item has a CTA: a block costs about 1.5 us, what a cut adds
+// (a second CTA's start, partial results, the merge) about 5
+constexpr int kWholeBlocks = 4;
 constexpr int kMaxSlots = 12;
 constexpr long long kTreeWait = kWaitLimitCycles;
 
@@ -575,8 +578,19 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
                    W = tree_ctas(gridDim.x, U, (unsigned)(p.batch * L.H * p.chunks), S.least == S.most);
     S.units = U;
     S.ctas = W;
-    const unsigned c = blockIdx.x;
-    tree_cursor(p, pre, c < W ? tree_unit(U, W, c) : U, c < W ? tree_unit(U, W, c + 1) : U, cur);
+    const unsigned c = blockIdx.x, hc = (unsigned)(L.H * p.chunks), items = (unsigned)p.batch * hc;
+    unsigned lo = U, hi = U;
+    if (items <= gridDim.x && S.most <= kWholeBlocks) {  // short items: a CTA each
+      if (c < items) {
+        const unsigned b = c / hc, n = (unsigned)(pre[b + 1] - pre[b]);
+        lo = (unsigned)pre[b] * hc + (c - b * hc) * n;
+        hi = lo + n;
+      }
+    } else if (c < W) {
+      lo = tree_unit(U, W, c);
+      hi = tree_unit(U, W, c + 1);
+    }
+    tree_cursor(p, pre, lo, hi, cur);
   }
   __syncwarp();
 
