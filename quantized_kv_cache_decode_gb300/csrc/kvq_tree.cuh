@@ -193,9 +193,10 @@ struct TreeShape {
   static constexpr uint32_t kPSwizzle = NT == 32 ? 4 : 2, kPMask = NT == 32 ? 3 : 7;
 };
 
-// Items of at most so many blocks are not cut where every item has a CTA: a block costs about 1.5 us, what a cut adds
-// (a second CTA's start, partial results, the merge) about 5
-constexpr int kWholeBlocks = 4;
+// Items of at most so many blocks are not cut where every item has a CTA: a block costs 1 to 1.5 us, what a cut adds (a
+// second CTA's start, partial results, the merge) about 10 (30 items of 5 to 8 blocks: 25 us cut, 17.6 us whole; items
+// of 27 blocks gain from the cut)
+constexpr int kWholeBlocks = 12;
 constexpr int kMaxSlots = 12;
 constexpr long long kTreeWait = kWaitLimitCycles;
 
