@@ -9,7 +9,10 @@
 // Bound by memory: every head is 256 bytes in and 256 bytes out.  Eight lanes hold a head,
 // two 16-byte pieces each (channels 8j.. and 64 + 8j..: both halves of its eight pairs), so
 // the sum of squares is three shuffles and the rotation none; a warp takes four heads at a
-// time.  The eight angles of a lane serve all heads of a token that its warp takes.
+// time and loads the next four meanwhile.  The eight angles of a lane serve all heads of a
+// token that its warp takes; a few tokens (a decode step) are spread over the SMs a warp per
+// four heads instead.  GB300: 32768 tokens of 64 + 16 heads 222 us, 6.05 TB/s (0.89 of a
+// measured copy); a step of 16 tokens 2.7 us in a captured graph.
 #include "kvq_common.cuh"
 
 namespace kvq {

@@ -16,21 +16,32 @@
 // operand fragment, which is also what tcgen05.st's 16x128b shape takes: dequantized
 // fragments go straight from registers to tensor memory.
 //
-// A CTA works on 128 cache tokens ("block") and NT = 32, 64 or 128 columns at a time:
-//   loader warp     cache bytes -> shared-memory slots (bulk copies; bf16 rows: cp.async)
+// A CTA works on 128 cache tokens ("block") and NT = 32, 64 or 128 columns at a time (the fewest that
+// hold all columns; chunks of 128 beyond that), its warps in roles joined by mbarriers:
+//   loader warp     cache bytes -> shared-memory slots, a block each (one bulk copy from a contiguous
+//                   store, one per block-table entry from a paged one; bf16 rows: cp.async)
+//   prep warps      (integer layers) a slot's fp32 scales and zero points -> f16 pairs, checked for range
 //   dequant warps   slots -> K and V^T as f16 in tensor memory, a warpgroup for each
 //   MMA warp        the tcgen05.mma of both products (scores of the next block before the outputs of this one)
-//   softmax warps   scores -> P (a warpgroup per half of the columns), running maximum and sum in fp32
-//   check warp      (integer layers) the scales of every slot: does f16 hold what they stand for
-// The blocks of all (sequence, kv head, column chunk) items are divided evenly over one
-// CTA per SM; an item cut between CTAs is merged by the last CTA to finish it, in CTA
-// order (the result does not depend on which one that is).
+//   softmax warps   scores -> P in one pass with the maxima so far, sums in fp32; a warpgroup for NT / 2
+//                   columns (NT / 4 of 128)
+// The blocks of all (sequence, kv head, column chunk) items are divided over one CTA per SM (tree_ctas);
+// an item cut between CTAs is merged by the last CTA to finish it, in CTA order (the result does not
+// depend on which one that is).
 //
-// Roundings: dequantized Keys and Values to f16 (codes of FP8 layers are exact in f16,
-// their scale enters in fp32), queries bf16 -> f16 (exact from 2^-14 up), P to f16, each
-// at most 2^-12 relative (2^-11 where half an f16 step is counted at the low end of a
-// binade); everything else is fp32.  A running maximum that is stale by at most 2^8 in
-// the exponent is kept (P then stays below 2^8, well inside f16).
+// What bounds it: neither HBM nor the tensor cores but the warps' instructions, about 8 cycles each for
+// the 5 to 7 warps of a scheduler (ncu, 16 sequences x 8 kv heads x 8192 INT4 tokens, 128 columns: issue
+// slots 55 % busy, tensor pipe 25 %, DRAM 17 %; 9000 warp instructions per block, of them about 3700
+// softmax, 3300 dequantization).  GB300, one launch: those 119 us (567 TFLOP/s, 0.30 of a measured bf16
+// GEMM); the same tokens in FP8 with 64 columns 71 us (3.87 TB/s, 0.57 of a measured copy); 128 heads of
+// 32768 INT2 tokens with 32 columns 290 us.
+//
+// Roundings.  The tensor cores take f16 operands, each half an f16 step (2^-11, relative) off at most: P,
+// the bf16 queries (exact from 2^-14 up), bf16 Keys and Values, and those of integer layers, s m + c with
+// an exact centred code m and s, c = s (2^(b-1) - z) rounded to f16 first.  (fp32 scales cost the
+// dequantization twice the instructions and gained a factor of 1.7 in the error.)  FP8 codes are exact in
+// f16; their tensor scales enter in fp32.  Sums, maxima and the merge are fp32.  A running maximum may be
+// stale by up to 8 in the exponent (P below 2^8, well inside f16).
 #pragma once
 
 #include <mutex>
@@ -169,8 +180,8 @@ constexpr int kBlk = 128;  // cache tokens per block
 template <int NT>
 struct TreeShape {
   // warps: 4 K, 4 V, then a softmax warpgroup per kSub columns, then loader, MMA, two prep warps.  128 columns take
-  // four softmax warpgroups (two of 64 columns each leave a scheduler too few warps to issue from: a 70B-shaped
-  // INT4 layer 152 -> 105 us), whose registers leave the others few
+  // four softmax warpgroups: two of 64 columns each leave a scheduler too few warps to issue from (152 -> 136 us for
+  // the 70B-shaped INT4 layer); their registers leave the others few.
   static constexpr int kGroups = NT == 128 ? 4 : 2, kSub = NT / kGroups;
   static constexpr int kSmWarps = 4 * kGroups, kIo = 8 + kSmWarps;
   static constexpr int kWarps = kIo + 4, kThreads = 32 * kWarps;
@@ -181,9 +192,8 @@ struct TreeShape {
   static constexpr int kQBytes = NT * 256;         // queries (f16): [two 64-channel halves][NT rows of 128 bytes]
   static constexpr int kPBytes = kBlk * NT * 2;    // one buffer of P (f16)
   static constexpr int kFixed = kQBytes + 2 * kPBytes;
-  // tensor memory: K and V twice 64 columns each, outputs NT, scores NT, twice where there is room (with 128
-  // columns one buffer of scores and two of K and V measured faster than the other way round, 8192-token INT4
-  // items of 128 columns: see the note on the roles' latencies above the kernel)
+  // tensor memory: K and V twice 64 columns each, outputs NT, scores NT, twice where there is room (128 columns: one
+  // buffer of scores and two of K and V; the other way round every dequantization waits for a product: 181 -> 172 us)
   static constexpr int kSb = NT == 128 ? 1 : 2;
   static constexpr uint32_t kTmK = 0, kTmV = 128, kTmS = 256, kTmO = 256 + kSb * NT;
   static_assert(kTmO + NT <= 512, "tensor memory");
