@@ -607,3 +607,121 @@ def test_decoding_steps(fmt):
                     O.append_token(caches[b][h], O.bf16_to_f32(kb[b, h, n]), O.bf16_to_f32(vb[b, h, n]))
                 TL.compare_logical(gl.logical(b, h, int(old[b] + ac[b])), caches[b][h])
     assert (seq.cpu().numpy() > np.array(lens) + 2).all()
+
+
+def test_tree_reads_blocks_beyond_4_gib():
+    # a pool of 420000 blocks (4.4 GB), the sequences' blocks scattered over it
+    H, g, N = 2, 2, 6
+    gl = TL.GpuLayer("int8", H, [333, 90], 16, 128, 16, 0, paged=True, seed=5, spare_blocks=420000)
+    assert gl.layer.sizes["block_pool"] > 1 << 32
+    table = gl.layer.block_table
+    used = table >= 0
+    table[used] = (gl.cfg.num_blocks - 1 - 7 * torch.arange(int(used.sum()), device="cuda")).int()
+    rng = np.random.default_rng(0)
+    kv = [[(I.random_bf16(10 * b + h, (T, 128)), I.random_bf16(50 + 10 * b + h, (T, 128))) for h in range(H)]
+          for b, T in enumerate(gl.lens)]
+    for b in range(2):
+        gl.append(b, np.stack([kv[b][h][0] for h in range(H)]), np.stack([kv[b][h][1] for h in range(H)]), 0)
+    caches = [[O.build_head_cache(O.bf16_to_f32(k), O.bf16_to_f32(v), gl.spec) for k, v in row] for row in kv]
+    q, k, v = draft_inputs(8, 2, H, g, N)
+    parents = np.stack([random_tree(rng, N, "random") for _ in range(2)])
+    ref, rlse, slack, lslack = S.decode_attention_tree(O.bf16_to_f32(q), caches, O.bf16_to_f32(k), O.bf16_to_f32(v), parents)
+    out, lse = tree_call(gl, q, k, v, parents)
+    assert gl.status_value() == 0
+    check_tree(out, lse, ref, rlse, slack)
+
+
+@pytest.mark.parametrize("lens", [[700] * 5, [5] * 40 + [1500], [130, 2000, 1, 0, 640, 90]])
+@pytest.mark.parametrize("fmt", ["int4", "fp8_e5m2"])
+def test_tree_work_split(fmt, lens):
+    # equal lengths (whole items), many short ones (a CTA each), ragged ones (cut and merged), with sequences of very
+    # different size side by side; two chunks of columns
+    H, g, N = 2, 8, 17
+    fp8 = fmt.startswith("fp8")
+    gl, caches = build(fmt, H, lens, 1 if fp8 else 32, 128, 0 if fp8 else 64, 1, False, len(lens))
+    rng = np.random.default_rng(4)
+    B = len(lens)
+    q, k, v = draft_inputs(40, B, H, g, N)
+    parents = np.stack([random_tree(rng, N, "random") for _ in range(B)])
+    ref, rlse, slack, lslack = S.decode_attention_tree(O.bf16_to_f32(q), caches, O.bf16_to_f32(k), O.bf16_to_f32(v), parents)
+    out, lse = tree_call(gl, q, k, v, parents)
+    assert gl.status_value() == 0
+    check_tree(out, lse, ref, rlse, slack)
+    worst = float((np.abs(lse.double().cpu().numpy() - rlse) / lslack).max())
+    assert worst <= 1, worst
+
+
+def test_calls_on_another_stream_and_in_a_graph():
+    # norm and rotation, verification and append on a side stream and captured: the results of the plain calls
+    B, n, hq, h, V = 3, 5, 8, 2, 3001
+    rng = np.random.default_rng(12)
+    rows = bf16_dev(I.random_bf16(1, (B * n, (hq + 2 * h) * 128)))
+    w = [bf16_dev(I.random_bf16(2 + i, (128,))) for i in range(2)]
+    pos = dev(rng.integers(0, 9000, (B, n)), torch.int32)
+    target, draft = (dev(softmax(2 * rng.standard_normal((B, n, V)))) for _ in range(2))
+    tokens, parents = dev(rng.integers(0, V, (B, n)), torch.int32), dev(np.tile(np.arange(n) - 1, (B, 1)), torch.int32)
+    u = dev(rng.random((B, n)).astype(F32))
+    gl, _ = build("int4", h, [100, 40, 63], 32, 128, 32, 0, False, 8, extra=n)
+    seq = gl.seq_lens_dev()
+    start = {k: t.clone() for k, t in gl.layer.buf.items() if t is not None}
+
+    def buffers():
+        bf = dict(dtype=torch.bfloat16, device="cuda")
+        i32 = dict(dtype=torch.int32, device="cuda")
+        return (torch.zeros(B, n, hq, 128, **bf), torch.zeros(B, h, n, 128, **bf), torch.zeros(B, h, n, 128, **bf),
+                torch.zeros(B, n, **i32), torch.zeros(B, **i32), torch.zeros(B, **i32))
+
+    def step(o, stream=None):
+        kvq.qk_norm_rope(rows, rows.shape[1], B, n, hq, h, *w, 1e-6, pos, 1e4, True, *o[:3], stream=stream)
+        kvq.verify_tree(target, V, draft, V, V, tokens, parents, u, n, B, *o[3:], gl.status, stream=stream)
+        kvq.append_accepted(gl.cfg, gl.layer.struct(), o[1], o[2], n, o[3], o[4], seq, B, gl.status, stream=stream)
+
+    def restore():
+        for k, t in start.items():
+            gl.layer.buf[k].copy_(t)
+        torch.cuda.synchronize()
+
+    want = buffers()
+    step(want)
+    torch.cuda.synchronize()
+    held = {k: gl.layer.buf[k].clone() for k in start}
+    restore()
+    side, o = torch.cuda.Stream(), buffers()
+    torch.cuda.synchronize()
+    step(o, side)
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(o, want)) and all(torch.equal(gl.layer.buf[k], t) for k, t in held.items())
+    restore()
+    graph, o = torch.cuda.CUDAGraph(), buffers()
+    with torch.cuda.graph(graph):
+        step(o)
+    for _ in range(2):
+        restore()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(o, want))
+        assert all(torch.equal(gl.layer.buf[k], t) for k, t in held.items())
+    assert gl.status_value() == 0
+
+
+def test_two_tree_calls_at_once():
+    # two streams, a workspace each, cut sequences of different size: each gets what it gets alone
+    H, g, N = 2, 4, 7
+    gl, caches = build("int4", H, [20000, 40, 6000], 32, 128, 32, 0, False, 21)
+    runs = []
+    for i, lens in enumerate(([20000, 40, 6000], [9000, 33, 1])):
+        q, k, v = draft_inputs(60 + i, 3, H, g, N)
+        parents = np.stack([random_tree(np.random.default_rng(10 * i + j), N, "random") for j in range(3)])
+        want, _ = tree_call(gl, q, k, v, parents, lens=lens)
+        size = kvq.decode_workspace_size_tree(gl.cfg, 3, N, H * g)
+        runs.append((want, [torch.zeros_like(want) for _ in range(8)], torch.zeros(size, dtype=torch.uint8, device="cuda"),
+                     size, (bf16_dev(q), bf16_dev(k), bf16_dev(v), dev(parents, torch.int32), gl.seq_lens_dev(lens)),
+                     torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for j in range(8):
+        for _, outs, ws, size, held, stream in runs:
+            kvq.decode_attention_tree(gl.cfg, gl.layer.struct(), *held[:4], N, H * g, held[4], 3, 1 / math.sqrt(128),
+                                      outs[j], False, None, ws, size, gl.status, stream)
+    torch.cuda.synchronize()
+    assert gl.status_value() == 0
+    assert all(torch.equal(o, want) for want, outs, *_ in runs for o in outs)
