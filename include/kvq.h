@@ -465,8 +465,9 @@ kvq_status kvq_selftest_bounded_wait(const kvq_layer_config* cfg, const kvq_laye
  *               (layers with pre-RoPE Keys)
  *   q_out       device bf16 [batch][n_tokens][num_q_heads][128]
  *   k_out, v_out  device bf16 [batch][num_kv_heads][n_tokens][128]; values are copied
- * All outputs 16-byte aligned, none overlapping qkv.  Computed in fp32 (angles
- * reduced exactly in 64-bit fixed point) and rounded once.
+ * All outputs 16-byte aligned, none overlapping qkv; at most 2^31 - 1 rows
+ * (KVQ_ERR_UNSUPPORTED).  Computed in fp32 (angles reduced exactly in 64-bit fixed
+ * point; a head whose squares leave fp32 is scaled first) and rounded once.
  */
 kvq_status kvq_qk_norm_rope(const void* qkv, int64_t row_stride, int32_t batch, int32_t n_tokens,
                             int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, const void* q_weight,
@@ -530,7 +531,8 @@ kvq_status kvq_decode_workspace_size_tree(const kvq_layer_config* cfg, int32_t b
  * none).  A w that is 0 everywhere at the end is replaced by the target row.
  * Sums are carried in pairs of fp32 numbers (about 45 bits) in a fixed order.  A
  * token outside [0, vocab) is not accepted (KVQ_DEV_BAD_TREE); a target row without
- * a positive finite sum gives next_token = -1 (KVQ_DEV_BAD_PROBS).
+ * a positive finite sum gives next_token = -1 (KVQ_DEV_BAD_PROBS).  vocab is at
+ * most 2^30 (KVQ_ERR_UNSUPPORTED).
  */
 kvq_status kvq_verify_tree(const float* target_probs, int64_t target_stride, const float* draft_probs,
                            int64_t draft_stride, int32_t vocab, const int32_t* tokens, const int32_t* parents,

@@ -86,9 +86,26 @@ __global__ void __launch_bounds__(32 * kRopeWarps) norm_rope_kernel(const __grid
       for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], fmaf(y[i], y[i], ss));
 #pragma unroll
       for (int o = 1; o < 8; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      // squares that leave fp32 (bf16 does not end at 2^64): such a head's sum again, of values scaled
+      // by a power of two that the quotient loses
+      float mean = ss * (1.0f / 128.0f) + p.eps;
+      const bool far = w && !(mean <= 0x1p100f && mean >= 0x1p-90f);
+      if (__any_sync(0xffffffffu, far)) {
+        const float s = !far ? 1.0f : (mean < 1.0f ? 0x1p100f : 0x1p-70f);
+        ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          x[i] *= s;
+          y[i] *= s;
+          ss = fmaf(x[i], x[i], fmaf(y[i], y[i], ss));
+        }
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        mean = ss * (1.0f / 128.0f) + p.eps * s * s;
+      }
       if (isq || isk) {
         if (w) {
-          const float r = 1.0f / sqrtf(ss * (1.0f / 128.0f) + p.eps);
+          const float r = 1.0f / sqrtf(mean);
           float u[8], v[8];
           bf16x8_to_f32(__ldg(w + j), u);
           bf16x8_to_f32(__ldg(w + 8 + j), v);

@@ -94,6 +94,41 @@ def test_qk_norm_rope(case):
             assert worst <= 0, (i, worst)
 
 
+@pytest.mark.parametrize("eps", [0.0, 1e-6])
+def test_qk_norm_rope_heads_whose_squares_leave_fp32(eps):
+    # values of 2^-130 to 2^126 next to ordinary ones in one warp: the formula's result, not 0 or infinity
+    hq, h, n = 6, 2, 40
+    rng = np.random.default_rng(3)
+    x = rng.standard_normal((n, hq + 2 * h, 128)).clip(-3, 3)
+    e = rng.choice([-130, -100, -60, -45, 0, 45, 64, 90, 126], (n, hq + 2 * h, 1))
+    xb = I.f32_to_bf16_bits((x * np.exp2(e.astype(np.float64)) * 0.5).astype(F32))
+    w = [I.f32_to_bf16_bits((1 + 0.3 * rng.standard_normal(128)).astype(F32)) for _ in range(2)]
+    pos = rng.integers(0, 5000, (1, n)).astype(np.int32)
+    q = torch.empty(1, n, hq, 128, dtype=torch.bfloat16, device="cuda")
+    k, v = (torch.empty(1, h, n, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    kvq.qk_norm_rope(bf16_dev(xb), (hq + 2 * h) * 128, 1, n, hq, h, *(bf16_dev(a) for a in w), eps, dev(pos), 1e4, True,
+                     q, k, v)
+    torch.cuda.synchronize()
+    xf = I.bf16_bits_to_f32(xb)
+    got = np.concatenate([q.double().cpu().numpy()[0], k.double().cpu().numpy()[0].transpose(1, 0, 2)], 1)
+    for i in range(hq + h):
+        y = S.head_norm(xf[:, i], I.bf16_bits_to_f32(w[i >= hq]), float(F32(eps)))
+        ref = S.rotate_exact(y, pos[0], 1e4)
+        mag = np.abs(y) + np.abs(np.roll(y, 64, -1))
+        # (half a step of a bf16 subnormal is 2^-134: outputs may be that small beside an eps)
+        tol = 2.0 ** -8 * np.abs(ref) + mag * (2.0 ** -20 + 2.0 ** -29 + 5000 * 2.0 ** -49) + 2.0 ** -134
+        assert (np.abs(got[:, i] - ref) <= tol).all(), (i, float((np.abs(got[:, i] - ref) / tol).max()))
+    assert np.array_equal(bits_of(v)[0].transpose(1, 0, 2), xb[:, hq + h:])
+
+
+def test_tree_workspace_of_the_largest_batch():
+    for fmt, G, Gv, R, kw in (("int8", 16, 16, 32, {}), ("int4", 32, 128, 32, {}), ("int2", 16, 16, 0, {}),
+                              ("fp8_e4m3", 1, 128, 0, {}), ("bf16", 0, 0, 0, {}), ("int8", 256, 16, 256, {})):
+        cfg = kvq.make_config(fmt, 1, G, Gv, R, 0, capacity_tokens=1024, **kw)
+        for n, hq in ((1, 1), (8, 8), (64, 8)):
+            assert kvq.decode_workspace_size_tree(cfg, 2048, n, hq) > 0, (fmt, n, hq)
+
+
 # --------------------------------------------------------------------------- #
 # tree attention
 # --------------------------------------------------------------------------- #
