@@ -684,6 +684,7 @@ kvq_status kvq_qk_norm_rope(const void* qkv, int64_t row_stride, int32_t batch, 
   if (!(eps >= 0.f) || !(eps < 3.0e38f)) return KVQ_ERR_INVALID_ARG;
   if (rotate_keys != 0 && rotate_keys != 1) return KVQ_ERR_INVALID_ARG;
   if (rope_base != 0.f && (!(rope_base > 1.f) || !(rope_base < 3.0e38f))) return KVQ_ERR_INVALID_ARG;
+  if ((int64_t)batch * n_tokens > 0x7FFFFFFFLL) return KVQ_ERR_UNSUPPORTED;
   if (batch == 0 || n_tokens == 0) return KVQ_OK;
   if (!qkv || !q_out || !k_out || !v_out || !aligned16(qkv) || !aligned16(q_out) || !aligned16(k_out) ||
       !aligned16(v_out) || (rope_base != 0.f && !positions))
@@ -728,6 +729,7 @@ kvq_status kvq_verify_tree(const float* target_probs, int64_t target_stride, con
                            const float* uniforms, int32_t n_nodes, int32_t batch, int32_t* path,
                            int32_t* n_accepted, int32_t* next_token, uint32_t* dev_status, void* stream) {
   if (vocab < 1 || n_nodes < 1 || n_nodes > kMaxNodes || batch < 0 || batch > kMaxBatch) return KVQ_ERR_INVALID_ARG;
+  if (vocab > (1 << 30)) return KVQ_ERR_UNSUPPORTED;  // (slices of a row are counted in 32 bits)
   if (target_stride < vocab || target_stride > ((int64_t)1 << 40)) return KVQ_ERR_INVALID_ARG;
   if (draft_probs && (draft_stride < vocab || draft_stride > ((int64_t)1 << 40))) return KVQ_ERR_INVALID_ARG;
   if (batch == 0) return KVQ_OK;
@@ -859,7 +861,7 @@ kvq_status kvq_decode_attention_tree(const kvq_layer_config* cfg, const kvq_laye
   p.Hq = num_q_heads;
   p.gh = num_q_heads / L.H;
   p.batch = batch;
-  p.most_tokens = (int)std::min<long long>(max_seq_tokens(L), 0x7FFFFFFFLL);
+  p.most_tokens = (int)std::min<long long>(max_seq_tokens(L), 0x7FFF0000LL);  // (a sequence and its tree fit 32 bits)
   p.chunks = G.chunks;
   p.nslots = G.nslots;
   p.slot_bytes = G.slot_bytes;

@@ -116,7 +116,7 @@ struct TreeParams {
   const int32_t* parents;  // [B][N]
   const int32_t* seq_lens;
   int N, Hq, gh, batch;
-  int most_tokens;  // that a sequence of the layer can hold (at most INT_MAX)
+  int most_tokens;  // that a sequence of the layer can hold (and 32 bits can count)
   int chunks;      // column chunks of NT per (sequence, kv head)
   int nslots, slot_bytes;
   int slot_hdr;    // bytes of a quantized slot before the block's own (integer layers: a record header)

@@ -30,7 +30,8 @@ ROPE = dict(qkv=4096, row_stride=12 * 128, batch=2, n_tokens=3, num_q_heads=8, n
     (dict(eps=float("nan")), -1), (dict(eps=float("inf")), -1), (dict(rope_base=1.0), -1),
     (dict(rope_base=float("nan")), -1), (dict(rotate_keys=2), -1), (dict(qkv=0), -1), (dict(qkv=4100), -1),
     (dict(q_out=0), -1), (dict(k_out=8), -1), (dict(v_out=0), -1), (dict(positions=None), -1),
-    (dict(q_weight=8194), -1), (dict(k_weight=8200), -1), (dict(head_dim=64), -2)])
+    (dict(q_weight=8194), -1), (dict(k_weight=8200), -1), (dict(head_dim=64), -2),
+    (dict(batch=1 << 16, n_tokens=1 << 15), -2)])
 def test_qk_norm_rope_refusals(kvq, bad, status):
     assert status_of(kvq, lambda: kvq.qk_norm_rope(**{**ROPE, **bad}, stream=0)) == status
 
@@ -50,6 +51,11 @@ VERIFY = dict(target_probs=16, target_stride=100, draft_probs=16, draft_stride=1
                                  dict(n_accepted=None), dict(next_token=None)])
 def test_verify_tree_refusals(kvq, bad):
     assert status_of(kvq, lambda: kvq.verify_tree(**{**VERIFY, **bad}, stream=0)) == -1
+
+
+def test_verify_tree_refuses_rows_beyond_its_counters(kvq):
+    wide = dict(vocab=(1 << 30) + 1, target_stride=1 << 31, draft_stride=1 << 31)
+    assert status_of(kvq, lambda: kvq.verify_tree(**{**VERIFY, **wide}, stream=0)) == -2
 
 
 def test_verify_tree_without_sequences_does_nothing(kvq):
