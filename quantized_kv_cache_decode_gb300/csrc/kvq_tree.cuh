@@ -613,6 +613,7 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
       int slot = 0;
       uint32_t ph = 1;  // the first pass over the slots finds them empty
       int used = 0;
+      unsigned rows = 0;  // slots that last held bf16 rows
       bool ok = true;
       // half-warps copy the K and the V row of a bf16 token
       const int kv = lane >> 4;
@@ -645,6 +646,10 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
             okmask = __reduce_or_sync(kAll, okmask);
             const uint32_t total = __reduce_add_sync(kAll, bytes + (pre ? (uint32_t)L.hdr_bytes : 0u));
             if (!(ok = tree_wait(&S.slot_empty[slot], ph, abort, p.status))) break;
+            if (F::kFp8 && (rows >> slot) & 1u) {  // those writes come before the bulk copy (integer layers: prep fences)
+              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+              rows &= ~(1u << slot);
+            }
             if (lane == 0) {
               S.slot_ok[slot] = okmask;
               mbar_arrive_expect_tx(bar, total);
@@ -696,6 +701,7 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
               asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
                                smem_addr(&S.slot_full[slot]))
                            : "memory");
+              rows |= 1u << slot;
               if (++slot == p.nslots) { slot = 0; ph ^= 1; }
               ++used;
             }
@@ -1225,7 +1231,7 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
               float rise = fmaxf(d, 0.f);
               if (!has) {
                 has = d != -INFINITY;
-                rise = has ? d : 0.f;
+                rise = has && d == d ? d : 0.f;  // (not a number: in the sum, where a merge keeps it)
               }
               neg[tok] -= rise;
               S.fall[j] = exp2_approx(-rise);

@@ -760,3 +760,20 @@ def test_two_tree_calls_at_once():
     torch.cuda.synchronize()
     assert gl.status_value() == 0
     assert all(torch.equal(o, want) for want, outs, *_ in runs for o in outs)
+
+
+def test_tree_query_that_is_not_a_number():
+    # a row of NaN gives NaN whether its sequence is cut over CTAs or not; the other rows keep their results
+    H, g, N = 1, 2, 4
+    gl, caches = build("int4", H, [6000, 70], 32, 128, 32, 0, False, 13)
+    q, k, v = draft_inputs(3, 2, H, g, N)
+    parents = np.tile([-1, 0, 1, 0], (2, 1))
+    want, wlse = tree_call(gl, q, k, v, parents)
+    q2 = q.copy()
+    q2[:, 2, 1] = 0x7FC0
+    out, lse = tree_call(gl, q2, k, v, parents)
+    assert gl.status_value() == kvq.DEV_RANGE
+    bad = torch.zeros(2, N, H * g, dtype=torch.bool, device="cuda")
+    bad[:, 2, 1] = True
+    assert out[bad].isnan().all() and lse[bad].isnan().all()
+    assert torch.equal(out[~bad], want[~bad]) and torch.equal(lse[~bad], wlse[~bad])
