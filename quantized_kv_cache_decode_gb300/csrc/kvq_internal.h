@@ -132,12 +132,12 @@ struct TreeParams {
   float* lse;
 };
 
-// CTAs that share a tree launch's blocks: whole items each where all are of one length and fill at
-// least 80 % of the grid that way (nothing is cut and merged), else all CTAs, at least one block each.
-__host__ __device__ inline unsigned tree_ctas(unsigned grid, unsigned blocks, unsigned items, bool equal) {
+// CTAs that share a tree launch's blocks: all, at least one block each; where items of one length go into CTAs without
+// remainder and cutting them would save a CTA at most `worth` blocks, as many as take whole items
+__host__ __device__ inline unsigned tree_ctas(unsigned grid, unsigned blocks, unsigned items, bool equal, unsigned worth) {
   if (equal && items > 0) {
     const unsigned k = (items + grid - 1) / grid, n = items / k;
-    if (n * k == items && n * 5 >= grid * 4) return n;
+    if (n * k == items && blocks / n - blocks / grid <= worth) return n;
   }
   return blocks < grid ? (blocks < 1 ? 1 : blocks) : grid;
 }

@@ -25,14 +25,14 @@
 //   MMA warp        the tcgen05.mma of both products (scores of the next block before the outputs of this one)
 //   softmax warps   scores -> P in one pass with the maxima so far, sums in fp32; a warpgroup for NT / 2
 //                   columns (NT / 4 of 128)
-// The blocks of all (sequence, kv head, column chunk) items are divided over one CTA per SM (tree_ctas);
-// an item cut between CTAs is merged by the last CTA to finish it, in CTA order (the result does not
+// The blocks of all (sequence, kv head, column chunk) items are divided over one CTA per SM, whole items
+// where a cut would save few blocks (kCutBlocks, tree_ctas); an item cut between CTAs is merged by the last CTA to finish it, in CTA order (the result does not
 // depend on which one that is).
 //
 // What bounds it: neither HBM nor the tensor cores but the warps' instructions, about 8 cycles each for
 // the 5 to 7 warps of a scheduler (ncu, 16 sequences x 8 kv heads x 8192 INT4 tokens, 128 columns: issue
 // slots 55 % busy, tensor pipe 25 %, DRAM 17 %; 9000 warp instructions per block, of them about 3700
-// softmax, 3300 dequantization).  GB300, one launch: those 119 us (567 TFLOP/s, 0.30 of a measured bf16
+// softmax, 3300 dequantization).  GB300, one launch: those 119 us (579 TFLOP/s, 0.31 of a measured bf16
 // GEMM); the same tokens in FP8 with 64 columns 71 us (3.87 TB/s, 0.57 of a measured copy); 128 heads of
 // 32768 INT2 tokens with 32 columns 290 us.
 //
@@ -201,12 +201,12 @@ struct TreeShape {
   // swizzle of that row length (B operand with the columns contiguous)
   static constexpr int kPRow = NT == 32 ? 64 : 128;
   static constexpr uint32_t kPSwizzle = NT == 32 ? 4 : 2, kPMask = NT == 32 ? 3 : 7;
+  // Blocks that a cut has to save a CTA before it pays (it costs partial results and the merge).  Break-even, GB300:
+  // 32 columns, 28 INT2 and 22 FP8 blocks; 64 columns, 14 of FP8; 128 columns, 16 to 20 of INT4 (32 and 128 items of
+  // 1280 to 49152 tokens; 128 FP8 items of 32768 tokens 248 us whole, 223 cut, of 8192 71 whole, 74 cut)
+  static constexpr unsigned kCutBlocks = NT == 32 ? 24 : 16;
 };
 
-// Items of at most so many blocks are not cut where every item has a CTA: a block costs 1 to 1.5 us, what a cut adds (a
-// second CTA's start, partial results, the merge) about 10 (30 items of 5 to 8 blocks: 25 us cut, 17.6 us whole; items
-// of 27 blocks gain from the cut)
-constexpr int kWholeBlocks = 12;
 constexpr int kMaxSlots = 12;
 constexpr long long kTreeWait = kWaitLimitCycles;
 
@@ -243,7 +243,7 @@ struct TreeSmem {  // small shared state, after the big buffers
   int par[64];
   unsigned units, ctas;           // blocks of the launch, CTAs that share them
   float kscale, vunit;            // FP8: the Keys' tensor scale, the unit of the Values (else 1)
-  int least, most;                // blocks of the shortest and the longest sequence
+  int whole;                      // an item a CTA
   TreeCursor cur[28];             // per warp
   TreeSeg seg[28];
 };
@@ -575,7 +575,12 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
     }
     least = __reduce_min_sync(kAll, least);
     most = __reduce_max_sync(kAll, most);
-    if (lane == 0) S.least = least, S.most = most;
+    if (lane == 0) {
+      const unsigned items = (unsigned)(p.batch * L.H * p.chunks), U = (unsigned)run * (unsigned)(L.H * p.chunks);
+      S.units = U;
+      S.whole = items <= gridDim.x && (unsigned)most <= U / gridDim.x + Sh::kCutBlocks;
+      S.ctas = tree_ctas(gridDim.x, U, items, least == most, Sh::kCutBlocks);
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -585,14 +590,10 @@ __global__ void __launch_bounds__(TreeShape<NT>::kThreads, 1) tree_kernel(const 
   TreeCursor& cur = S.cur[warp];
   TreeSeg& sg = S.seg[warp];
   if (lane == 0) {
-    const unsigned U = (unsigned)pre[p.batch] * (unsigned)(L.H * p.chunks),
-                   W = tree_ctas(gridDim.x, U, (unsigned)(p.batch * L.H * p.chunks), S.least == S.most);
-    S.units = U;
-    S.ctas = W;
-    const unsigned c = blockIdx.x, hc = (unsigned)(L.H * p.chunks), items = (unsigned)p.batch * hc;
+    const unsigned U = S.units, W = S.ctas, c = blockIdx.x, hc = (unsigned)(L.H * p.chunks);
     unsigned lo = U, hi = U;
-    if (items <= gridDim.x && S.most <= kWholeBlocks) {  // short items: a CTA each
-      if (c < items) {
+    if (S.whole) {  // an item a CTA
+      if (c < (unsigned)p.batch * hc) {
         const unsigned b = c / hc, n = (unsigned)(pre[b + 1] - pre[b]);
         lo = (unsigned)pre[b] * hc + (c - b * hc) * n;
         hi = lo + n;
