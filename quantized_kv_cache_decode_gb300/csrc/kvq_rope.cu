@@ -11,7 +11,7 @@
 // the sum of squares is three shuffles and the rotation none; a warp takes four heads at a
 // time and loads the next four meanwhile.  The eight angles of a lane serve all heads of a
 // token that its warp takes; a few tokens (a decode step) are spread over the SMs a warp per
-// four heads instead.  GB300: 32768 tokens of 64 + 16 heads 222 us, 6.05 TB/s (0.89 of a
+// four heads instead.  GB300: 32768 tokens of 64 + 16 heads 224 us, 6.0 TB/s (0.88 of a
 // measured copy); a step of 16 tokens 2.7 us in a captured graph.
 #include "kvq_common.cuh"
 

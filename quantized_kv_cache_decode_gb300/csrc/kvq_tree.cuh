@@ -26,15 +26,15 @@
 //   softmax warps   scores -> P in one pass with the maxima so far, sums in fp32; a warpgroup for NT / 2
 //                   columns (NT / 4 of 128)
 // The blocks of all (sequence, kv head, column chunk) items are divided over one CTA per SM, whole items
-// where a cut would save few blocks (kCutBlocks, tree_ctas); an item cut between CTAs is merged by the last CTA to finish it, in CTA order (the result does not
-// depend on which one that is).
+// where a cut would save few blocks (kCutBlocks, tree_ctas); an item cut between CTAs is merged by the
+// last CTA to finish it, in CTA order (the result does not depend on which one that is).
 //
 // What bounds it: neither HBM nor the tensor cores but the warps' instructions, about 8 cycles each for
 // the 5 to 7 warps of a scheduler (ncu, 16 sequences x 8 kv heads x 8192 INT4 tokens, 128 columns: issue
 // slots 55 % busy, tensor pipe 25 %, DRAM 17 %; 9000 warp instructions per block, of them about 3700
 // softmax, 3300 dequantization).  GB300, one launch: those 119 us (579 TFLOP/s, 0.31 of a measured bf16
 // GEMM); the same tokens in FP8 with 64 columns 71 us (3.87 TB/s, 0.57 of a measured copy); 128 heads of
-// 32768 INT2 tokens with 32 columns 290 us.
+// 32768 INT2 tokens with 32 columns 293 us.
 //
 // Roundings.  The tensor cores take f16 operands, each half an f16 step (2^-11, relative) off at most: P,
 // the bf16 queries (exact from 2^-14 up), bf16 Keys and Values, and those of integer layers, s m + c with
