@@ -31,7 +31,7 @@
 //
 // What bounds it: neither HBM nor the tensor cores but the warps' instructions, about 8 cycles each for
 // the 5 to 7 warps of a scheduler (ncu, 16 sequences x 8 kv heads x 8192 INT4 tokens, 128 columns: issue
-// slots 55 % busy, tensor pipe 25 %, DRAM 17 %; 9000 warp instructions per block, of them about 3700
+// slots 61 % busy, tensor pipe 29 %, DRAM 16 %; 8600 warp instructions per block, of them about 3700
 // softmax, 3300 dequantization).  GB300, one launch: those 119 us (579 TFLOP/s, 0.31 of a measured bf16
 // GEMM); the same tokens in FP8 with 64 columns 71 us (3.87 TB/s, 0.57 of a measured copy); 128 heads of
 // 32768 INT2 tokens with 32 columns 293 us.
